@@ -463,6 +463,167 @@ moe_status moe_fp8_prepack(int32_t N, int32_t K, const uint8_t *w_canonical, uin
                            void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* W8A8: products in 8-bit integers with one scale per token and one per     */
+/* output channel, next to the 4-bit experts and the FP8_BLOCK projection.   */
+/*   acc[m][n] = sum_k a[m][k] * w[n][k]      exact, in int32                */
+/*   out[m][n] = bf16( acc * a_scales[m] * w_scales[n] )                     */
+/* The sum is exact whatever its order, so the dense, the grouped and the    */
+/* one-launch forms give the same bits for the same codes and scales.        */
+
+/* Quantisation of each row by itself, symmetric: with amax = max |a[r][k]|  */
+/*   scales[r]   = amax / 127 (fp32, rounded to nearest)                     */
+/*   codes[r][k] = the integer nearest 127 a[r][k] / amax, ties to even, in  */
+/*                 [-127, 127] (exactly: the quotient is not rounded first)  */
+/* A row of zeros gets scale 0 and codes 0; a row that holds an infinity or  */
+/* a NaN gets scale NaN and codes 0 (its products are NaN, other rows'       */
+/* unaffected).  Weights [N][K] quantise per output channel with the same    */
+/* call.                                                                     */
+/*   rows   0..MOE_MAX_TOKENS*9;  K multiple of 16, 16..65536                */
+/*   a      bf16 [rows][K], 16-byte aligned                                  */
+/*   codes  int8 [rows][K] (written), 16-byte aligned                        */
+/*   scales fp32 [rows] (written)                                            */
+moe_status moe_act_quant_int8(int32_t rows, int32_t K, const uint16_t *a, int8_t *codes,
+                              float *scales, void *stream);
+
+/* Canonical INT8 weights [n_groups][N][K] into the layout of the products:  */
+/* 1 KB blocks of 16 weight rows x 64 k; block (t, kb) of group g at         */
+/* ((g*NT + t)*KB + kb)*1024 with NT = 4*ceil(N/64), KB = 2*ceil(K/128).     */
+/* Lane l owns bytes [16l, 16l+16): k = 64kb + 16(l/16) + [0,16) of the row  */
+/* n = 64(t/4) + 16((l%16)/4) + 4(t%4) + l%4.  Rows past N and k past K are  */
+/* zeros.  Codes may take every int8 value, -128 included.                   */
+/*   n_groups   1..257;  N, K multiples of 16, 16..65536                     */
+/*   w_canonical int8 [n_groups][N][K]; w_packed moe_w8a8_packed_bytes       */
+/*              bytes (0 when a size is invalid); both 16-byte aligned, not  */
+/*              overlapping                                                  */
+size_t moe_w8a8_packed_bytes(int32_t n_groups, int32_t N, int32_t K);
+moe_status moe_w8a8_prepack(int32_t n_groups, int32_t N, int32_t K, const int8_t *w_canonical,
+                            int8_t *w_packed, void *stream);
+
+/* Dense product on quantised rows.                                          */
+/*   M          0..MOE_MAX_TOKENS;  N, K multiples of 16, 16..65536          */
+/*   a, a_scales  int8 [M][K] (16-byte aligned), fp32 [M], as written by     */
+/*              moe_act_quant_int8 (-128 is allowed too)                     */
+/*   w_packed   one group in the layout of moe_w8a8_prepack, 16-byte aligned */
+/*   w_scales   fp32 [N], 16-byte aligned                                    */
+/*   out        bf16 [M][N], 16-byte aligned                                 */
+moe_status moe_w8a8_gemm(int32_t M, int32_t N, int32_t K, const int8_t *a, const float *a_scales,
+                         const int8_t *w_packed, const float *w_scales, uint16_t *out,
+                         void *stream);
+
+/* moe_act_quant_int8 followed by moe_w8a8_gemm, with the same bits in out;  */
+/* up to 16 rows with K <= 4096 it is one launch, which quantises each row   */
+/* where it is used.                                                         */
+/*   x          bf16 [M][K], 16-byte aligned                                 */
+/*   codes, scales  scratch: int8 [M][K] (16-byte aligned) and fp32 [M];     */
+/*              their contents afterwards are unspecified                    */
+/*   the rest as moe_w8a8_gemm                                               */
+moe_status moe_w8a8_linear(int32_t M, int32_t N, int32_t K, const uint16_t *x,
+                           const int8_t *w_packed, const float *w_scales, int8_t *codes,
+                           float *scales, uint16_t *out, void *stream);
+
+/* The grouped product over the permuted rows, as moe_w4a16_grouped_gemm,    */
+/* with INT8 weights: out = bf16(acc * a_scale * w_scale) (MOE_ACT_NONE) or  */
+/* bf16(silu(gate) * up) of the scaled halves (MOE_ACT_SWIGLU).              */
+/*   a, a_scales  int8 [n_src][K] and fp32 [n_src] (with a_gather) or [R][K] */
+/*              and [R]; a 16-byte aligned                                   */
+/*   a_gather, n_src, group_offsets: as moe_w4a16_grouped_gemm (a row whose  */
+/*              source lies outside [0, n_src) is written as zeros)          */
+/*   N, K       multiples of 16, 16..65536; N a multiple of 128 for SwiGLU   */
+/*   w_packed   G groups in the layout of moe_w8a8_prepack, 16-byte aligned  */
+/*   w_scales   fp32 [G][N], 16-byte aligned                                 */
+/*   out        bf16 [R][N] (NONE) or [R][N/2] (SWIGLU), 16-byte aligned     */
+moe_status moe_w8a8_grouped_gemm(const moe_layer_desc *desc, int32_t T, const int8_t *a,
+                                 const float *a_scales, const int32_t *a_gather, int32_t n_src,
+                                 int32_t N, int32_t K, const int8_t *w_packed,
+                                 const float *w_scales, const int32_t *group_offsets, int32_t act,
+                                 uint16_t *out, void *stream);
+
+/* Everything after the routing for experts in INT8, in one call: quantise   */
+/* x, gate/up product with SwiGLU into h, quantise h, down product into y,   */
+/* moe_combine into out.  The same bits as those calls one after the other   */
+/* (up to 16 tokens the products quantise their rows themselves: three       */
+/* launches instead of five).                                                */
+/*   x          bf16 [T][H]; topk_w, group_offsets, sorted_token,            */
+/*              row_of_slot as written by moe_route_permute                  */
+/*   w13_packed, w13_scales  G groups of [2I][H] (gate rows, then up rows)   */
+/*              in the layout of moe_w8a8_prepack, fp32 [G][2I]              */
+/*   w2_packed, w2_scales    G groups of [H][I], fp32 [G][H]                 */
+/*   xq, xqs    scratch int8 [T][H], fp32 [T] (unspecified afterwards)       */
+/*   h          bf16 [R][I] (written)                                        */
+/*   hq, hqs    scratch int8 [R][I], fp32 [R] (unspecified afterwards)       */
+/*   y          bf16 [R][H] (written); out bf16 [T][H] (written)             */
+/* 16-byte aligned: x, w13_packed, w13_scales, w2_packed, w2_scales, xq, h,  */
+/* hq, y, out.                                                               */
+moe_status moe_w8a8_experts(const moe_layer_desc *desc, int32_t T, const uint16_t *x,
+                            const float *topk_w, const int32_t *group_offsets,
+                            const int32_t *sorted_token, const int32_t *row_of_slot,
+                            const int8_t *w13_packed, const float *w13_scales,
+                            const int8_t *w2_packed, const float *w2_scales, int8_t *xq,
+                            float *xqs, uint16_t *h, int8_t *hq, float *hqs, uint16_t *y,
+                            uint16_t *out, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Balance of the router: how many tokens each expert gets, a loss that     */
+/* grows with the imbalance, and the gradient of the router's logits.        */
+/* With the scores of moe_route, s[t][e] = sigmoid(logits[t][e]) (to fp32    */
+/* rounding; below 2^-126 they count as 0), and                              */
+/* p[t][e] = s[t][e] / sum_j s[t][j] (0 when every score of the token is 0), */
+/* for the packed sequences q = [seq_offsets[q], seq_offsets[q+1]) with n_q  */
+/* live tokens (those whose token_mask is not 0):                            */
+/*   counts[q][e]    = number of (t, j), t live in q, topk_idx[t][j] = e     */
+/*   prob_sums[q][e] = sum over t live in q of p[t][e]                       */
+/*   seq_coef[q]     = alpha E / (k n_q^2 Q'), Q' = number of sequences with */
+/*                     n_q > 0; 0 when n_q = 0                               */
+/*   loss            = sum_q seq_coef[q] sum_e counts[q][e] prob_sums[q][e]  */
+/* (alpha when the tokens of every sequence are spread evenly.)  Tokens that */
+/* are masked or lie outside every sequence take no part, whatever their     */
+/* logits hold (NaN included).  Sums are fp32 in a fixed order (the same     */
+/* bits every call), the final sum in fp64.                                  */
+/*   T            0..MOE_MAX_TOKENS; T = 0 writes zeros to every output      */
+/*   n_seq        1..MOE_MAX_TOKENS                                          */
+/*   seq_offsets  int32 [n_seq+1], non-decreasing, in [0, T] (values outside */
+/*                give unspecified results, in bounds); NULL with n_seq = 1: */
+/*                one sequence of all T tokens                               */
+/*   token_mask   uint8 [T], or NULL: every token is live                    */
+/*   logits       fp32 [T][E]; topk_idx int32 [T][k] (ids outside [0, E) are */
+/*                not counted), as written by moe_route                      */
+/*   alpha        finite                                                     */
+/*   counts       int32 [n_seq][E]; prob_sums fp32 [n_seq][E]; seq_coef fp32 */
+/*                [n_seq]; loss fp32 [1] (all written)                       */
+/*   ws, ws_bytes workspace of moe_balance_workspace_bytes(desc, T, n_seq)   */
+/*                bytes, 16-byte aligned, zero before the first call (every  */
+/*                call leaves its counter zero); calls that may overlap in   */
+/*                time need distinct workspaces                              */
+/* Of desc only n_routed and top_k matter here (and routed_scale below).     */
+size_t moe_balance_workspace_bytes(const moe_layer_desc *desc, int32_t T, int32_t n_seq);
+moe_status moe_balance_loss(const moe_layer_desc *desc, int32_t T, int32_t n_seq,
+                            const int32_t *seq_offsets, const uint8_t *token_mask,
+                            const float *logits, const int32_t *topk_idx, float alpha,
+                            int32_t *counts, float *prob_sums, float *seq_coef, float *loss,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of the router's logits, from that of the balance loss and that   */
+/* of the routing weights w[t][j] = routed_scale s[t][i_j] / sum_l s[t][i_l] */
+/* (i_j = topk_idx[t][j]; the selection itself has no gradient):             */
+/*   c[e]  = d_loss * seq_coef[q] * counts[q][e]       (q: the sequence of t) */
+/*   ds[e] = (c[e] - sum_j c[j] p[j]) / sum_j s[j]                           */
+/*         + sum over j with i_j = e of routed_scale (d_topk_w[t][j]         */
+/*             - sum_l d_topk_w[t][l] s[i_l] / S) / S,   S = sum_l s[i_l]    */
+/*   d_logits[t][e] = ds[e] s[e] (1 - s[e]);  rows that are not live: zeros  */
+/* (a term whose sum of scores is 0 is left out).                            */
+/*   seq_offsets, token_mask, logits, topk_idx: as moe_balance_loss          */
+/*   counts, seq_coef  as written by moe_balance_loss                        */
+/*   d_loss       fp32 [1], or NULL: no balance term (counts and seq_coef    */
+/*                may then be NULL too)                                      */
+/*   d_topk_w     fp32 [T][k], or NULL: no routing-weight term               */
+/*   d_logits     fp32 [T][E] (written)                                      */
+moe_status moe_route_backward(const moe_layer_desc *desc, int32_t T, int32_t n_seq,
+                              const int32_t *seq_offsets, const uint8_t *token_mask,
+                              const float *logits, const int32_t *topk_idx, const int32_t *counts,
+                              const float *seq_coef, const float *d_loss, const float *d_topk_w,
+                              float *d_logits, void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* Weight layout.                                                             */
 /* Canonical layout (what a checkpoint holds): codes [G][N][K/2] bytes, byte  */
 /* c of a row holds element 2c in its low nibble and 2c+1 in its high nibble, */

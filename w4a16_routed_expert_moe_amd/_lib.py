@@ -36,7 +36,9 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_permute", "moe_route_permute
            "moe_w4a16_down_combine", "moe_w4a16_decode_token", "moe_w4a16_decode_token_supported", "moe_combine", "moe_w4a16_prepack", "moe_gen_int4_codes", "moe_gen_fp16_scales",
            "moe_mxfp4_grouped_gemm", "moe_mxfp4_prepack", "moe_gen_ue8m0_scales", "moe_mxfp4_decode_token", "moe_w4a8_decode_token",
            "moe_act_quant_fp8", "moe_act_quant_fp8_dequant", "moe_w4a8_grouped_gemm", "moe_fp8_block_gemm", "moe_fp8_prepack",
-           "moe_status_str", "moe_abi_version")
+           "moe_act_quant_int8", "moe_w8a8_packed_bytes", "moe_w8a8_prepack", "moe_w8a8_gemm", "moe_w8a8_linear",
+           "moe_w8a8_grouped_gemm", "moe_w8a8_experts", "moe_balance_workspace_bytes", "moe_balance_loss",
+           "moe_route_backward", "moe_status_str", "moe_abi_version")
 
 
 class MoeError(RuntimeError):
@@ -100,6 +102,14 @@ def lib() -> ctypes.CDLL:
             "moe_w4a8_grouped_gemm": [D, i32, P, P, P, i32, i32, i32, P, P, P, i32, P, P],
             "moe_fp8_block_gemm": [i32, i32, i32, P, P, P, P, P, P],
             "moe_fp8_prepack": [i32, i32, P, P, P],
+            "moe_act_quant_int8": [i32, i32, P, P, P, P],
+            "moe_w8a8_prepack": [i32, i32, i32, P, P, P],
+            "moe_w8a8_gemm": [i32, i32, i32, P, P, P, P, P, P],
+            "moe_w8a8_linear": [i32, i32, i32, P, P, P, P, P, P, P],
+            "moe_w8a8_grouped_gemm": [D, i32, P, P, P, i32, i32, i32, P, P, P, i32, P, P],
+            "moe_w8a8_experts": [D, i32, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P],
+            "moe_balance_loss": [D, i32, i32, P, P, P, P, ctypes.c_float, P, P, P, P, P, SZ, P],
+            "moe_route_backward": [D, i32, i32, P, P, P, P, P, P, P, P, P, P],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -107,6 +117,10 @@ def lib() -> ctypes.CDLL:
             fn.restype = ctypes.c_int
         L.moe_workspace_bytes.argtypes = [D, i32]
         L.moe_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_w8a8_packed_bytes.argtypes = [i32, i32, i32]
+        L.moe_w8a8_packed_bytes.restype = ctypes.c_size_t
+        L.moe_balance_workspace_bytes.argtypes = [D, i32, i32]
+        L.moe_balance_workspace_bytes.restype = ctypes.c_size_t
         L.moe_status_str.argtypes = [ctypes.c_int]
         L.moe_status_str.restype = ctypes.c_char_p
         L.moe_abi_version.argtypes = []
@@ -414,3 +428,101 @@ def moe_fp8_prepack(N: int, K: int, w_canonical, w_packed, stream=None):
     _check("moe_fp8_prepack", lib().moe_fp8_prepack(
         N, K, _ptr(w_canonical, "w_canonical", torch.uint8, N * K), _ptr(w_packed, "w_packed", torch.uint8, N * K),
         _stream(stream)))
+
+
+# ------------------------------------------------------------------ W8A8
+def moe_act_quant_int8(rows: int, K: int, a, codes, scales, stream=None):
+    _check("moe_act_quant_int8", lib().moe_act_quant_int8(
+        rows, K, _ptr(a, "a", torch.bfloat16, rows * K), _ptr(codes, "codes", torch.int8, rows * K),
+        _ptr(scales, "scales", torch.float32, rows), _stream(stream)))
+
+
+def moe_w8a8_packed_bytes(n_groups: int, N: int, K: int) -> int:
+    """Bytes of the packed weights of n_groups matrices [N][K] (0 when a size is invalid)."""
+    return int(lib().moe_w8a8_packed_bytes(n_groups, N, K))
+
+
+def moe_w8a8_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stream=None):
+    _check("moe_w8a8_prepack", lib().moe_w8a8_prepack(
+        n_groups, N, K, _ptr(w_canonical, "w_canonical", torch.int8, n_groups * N * K),
+        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(n_groups, N, K)), _stream(stream)))
+
+
+def moe_w8a8_gemm(M: int, N: int, K: int, a, a_scales, w_packed, w_scales, out, stream=None):
+    _check("moe_w8a8_gemm", lib().moe_w8a8_gemm(
+        M, N, K, _ptr(a, "a", torch.int8, M * K), _ptr(a_scales, "a_scales", torch.float32, M),
+        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(1, N, K)),
+        _ptr(w_scales, "w_scales", torch.float32, N), _ptr(out, "out", torch.bfloat16, M * N), _stream(stream)))
+
+
+def moe_w8a8_linear(M: int, N: int, K: int, x, w_packed, w_scales, codes, scales, out, stream=None):
+    """moe_act_quant_int8 + moe_w8a8_gemm in one call; codes and scales are scratch."""
+    _check("moe_w8a8_linear", lib().moe_w8a8_linear(
+        M, N, K, _ptr(x, "x", torch.bfloat16, M * K),
+        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(1, N, K)),
+        _ptr(w_scales, "w_scales", torch.float32, N), _ptr(codes, "codes", torch.int8, M * K),
+        _ptr(scales, "scales", torch.float32, M), _ptr(out, "out", torch.bfloat16, M * N), _stream(stream)))
+
+
+def moe_w8a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_src: int, N: int, K: int,
+                          w_packed, w_scales, group_offsets, act: int, out, stream=None):
+    G, R = desc.groups, desc.rows(T)
+    a_rows = n_src if a_gather is not None else R
+    out_cols = N // 2 if act == MOE_ACT_SWIGLU else N
+    _check("moe_w8a8_grouped_gemm", lib().moe_w8a8_grouped_gemm(
+        ctypes.byref(desc), T, _ptr(a, "a", torch.int8, a_rows * K),
+        _ptr(a_scales, "a_scales", torch.float32, a_rows),
+        _ptr(a_gather, "a_gather", torch.int32, R, optional=True), n_src, N, K,
+        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(G, N, K)),
+        _ptr(w_scales, "w_scales", torch.float32, G * N),
+        _ptr(group_offsets, "group_offsets", torch.int32, G + 1), act,
+        _ptr(out, "out", torch.bfloat16, R * out_cols), _stream(stream)))
+
+
+def moe_w8a8_experts(desc: MoeLayerDesc, T: int, x, topk_w, group_offsets, sorted_token, row_of_slot, w13_packed,
+                     w13_scales, w2_packed, w2_scales, xq, xqs, h, hq, hqs, y, out, stream=None):
+    """Everything after the routing for INT8 experts; xq, xqs, hq and hqs are scratch."""
+    H, I, G, R, S = desc.hidden, desc.inter, desc.groups, desc.rows(T), desc.top_k + desc.n_shared
+    _check("moe_w8a8_experts", lib().moe_w8a8_experts(
+        ctypes.byref(desc), T, _ptr(x, "x", torch.bfloat16, T * H),
+        _ptr(topk_w, "topk_w", torch.float32, T * desc.top_k),
+        _ptr(group_offsets, "group_offsets", torch.int32, G + 1),
+        _ptr(sorted_token, "sorted_token", torch.int32, R), _ptr(row_of_slot, "row_of_slot", torch.int32, T * S),
+        _ptr(w13_packed, "w13_packed", torch.int8, moe_w8a8_packed_bytes(G, 2 * I, H)),
+        _ptr(w13_scales, "w13_scales", torch.float32, G * 2 * I),
+        _ptr(w2_packed, "w2_packed", torch.int8, moe_w8a8_packed_bytes(G, H, I)),
+        _ptr(w2_scales, "w2_scales", torch.float32, G * H), _ptr(xq, "xq", torch.int8, T * H),
+        _ptr(xqs, "xqs", torch.float32, T), _ptr(h, "h", torch.bfloat16, R * I),
+        _ptr(hq, "hq", torch.int8, R * I), _ptr(hqs, "hqs", torch.float32, R),
+        _ptr(y, "y", torch.bfloat16, R * H), _ptr(out, "out", torch.bfloat16, T * H), _stream(stream)))
+
+
+# ------------------------------------------------------------------ router balance and gradient
+def moe_balance_workspace_bytes(desc: MoeLayerDesc, T: int, n_seq: int) -> int:
+    """Bytes of the workspace moe_balance_loss needs (0 when a size is invalid)."""
+    return int(lib().moe_balance_workspace_bytes(ctypes.byref(desc), T, n_seq))
+
+
+def moe_balance_loss(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_mask, logits, topk_idx, alpha: float,
+                     counts, prob_sums, seq_coef, loss, ws, stream=None):
+    E, k = desc.n_routed, desc.top_k
+    _check("moe_balance_loss", lib().moe_balance_loss(
+        ctypes.byref(desc), T, n_seq, _ptr(seq_offsets, "seq_offsets", torch.int32, n_seq + 1, optional=True),
+        _ptr(token_mask, "token_mask", torch.uint8, T, optional=True), _ptr(logits, "logits", torch.float32, T * E),
+        _ptr(topk_idx, "topk_idx", torch.int32, T * k), alpha, _ptr(counts, "counts", torch.int32, n_seq * E),
+        _ptr(prob_sums, "prob_sums", torch.float32, n_seq * E), _ptr(seq_coef, "seq_coef", torch.float32, n_seq),
+        _ptr(loss, "loss", torch.float32, 1), *_ws(ws), _stream(stream)))
+
+
+def moe_route_backward(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_mask, logits, topk_idx, counts,
+                       seq_coef, d_loss, d_topk_w, d_logits, stream=None):
+    E, k = desc.n_routed, desc.top_k
+    _check("moe_route_backward", lib().moe_route_backward(
+        ctypes.byref(desc), T, n_seq, _ptr(seq_offsets, "seq_offsets", torch.int32, n_seq + 1, optional=True),
+        _ptr(token_mask, "token_mask", torch.uint8, T, optional=True), _ptr(logits, "logits", torch.float32, T * E),
+        _ptr(topk_idx, "topk_idx", torch.int32, T * k),
+        _ptr(counts, "counts", torch.int32, n_seq * E, optional=d_loss is None),
+        _ptr(seq_coef, "seq_coef", torch.float32, n_seq, optional=d_loss is None),
+        _ptr(d_loss, "d_loss", torch.float32, 1, optional=True),
+        _ptr(d_topk_w, "d_topk_w", torch.float32, T * k, optional=True),
+        _ptr(d_logits, "d_logits", torch.float32, T * E), _stream(stream)))

@@ -1,0 +1,233 @@
+// moe_w8a8_tiled.hip -- the W8A8 product for many rows per group: tiles of up
+// to 16 MC permuted rows by 64 NSW weight rows, four waves side by side along
+// the weight rows.
+//
+// Per 128-wide k step the tile's activation codes (128 bytes a row) go from
+// global memory straight into one of three LDS stages, a step and a half
+// ahead, and every wave reads all of them; the weights, which no two waves of
+// a workgroup share, go from global memory into registers, one to two half
+// steps (64 k) ahead, so that per matrix instruction of 16 cycles only
+// 1024 / NSW bytes come out of LDS.  The sums are exact in int32, so the k
+// loop holds nothing but loads and matrix instructions; both scales are
+// applied in the epilogue.
+// The wave multiplies only the m-tiles (16 rows) that have rows: the count is
+// a constant of each instance of the k loop, chosen once per work item.
+#include <type_traits>
+
+#include "moe_w8a8.h"
+
+namespace moe {
+namespace w8 {
+namespace {
+
+constexpr int kStages = 3;
+
+// Chunk c (16 bytes) of row r of a stage sits at chunk c ^ swz(r): the eight
+// rows of each parity that one 16-lane group of an operand read takes then
+// lie on eight distinct chunks (two 128-byte rows share the 64 banks).
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// The matrix instruction written as assembly, so that each accumulator stays
+// in its registers: with all 256 accumulation registers in use the compiler's
+// own form rotates the accumulators through copies.  The two wait states in
+// front cover a copy that the compiler may place before it (they pass in the
+// shadow of the previous instruction's 16 cycles); an accumulator comes up
+// again only after every other one, and mfma_drain precedes the first use of
+// the sums.
+__device__ __forceinline__ void mfma_acc(v4i &acc, u32x4 a, u32x4 b) {
+    asm volatile("s_nop 1\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma_drain() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
+template <int ACT, int NSW, int MC>
+__global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
+    constexpr int TM = 16 * MC;  // times 64 NSW weight rows
+    constexpr int HSW = NSW / 2;
+    __shared__ u32x4 sA[kStages * TM * 8];
+    __shared__ int srow[TM];
+    if constexpr (NSW * MC >= 64) asm volatile("" ::: "a0");
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id();
+    const int m = l & 15, q = l >> 4;
+    TileItem it;
+    if (!workgroup_tile_item(p.NB, TM, p.offsets, p.G, p.R, it)) return;
+    const int K = p.K, KB = p.KB, KG = KB >> 1, NTH = p.NT >> 1;
+    if (tid < TM) {
+        int sr = -1;
+        if (tid < it.mrows) {
+            sr = it.m0 + tid;
+            if (p.gather) {
+                const int t = p.gather[it.m0 + tid];
+                sr = (unsigned)t < (unsigned)p.n_src ? t : -1;
+            }
+        }
+        srow[tid] = sr;
+    }
+    __syncthreads();
+    const int mc = (it.mrows + 15) >> 4;  // m-tiles that have rows
+
+    // the wave's subtiles: NSW consecutive ones, or (SwiGLU) NSW/2 of the
+    // gate projection and the same of the up projection
+    auto tile_of = [&](int j) {
+        if (ACT == MOE_ACT_SWIGLU)
+            return (j < HSW ? 0 : NTH) + min((it.nb * 4 + wave) * HSW + (j < HSW ? j : j - HSW), NTH - 1);
+        return min((it.nb * 4 + wave) * NSW + j, p.NT - 1);
+    };
+    const int8_t *wb[NSW];
+#pragma unroll
+    for (int j = 0; j < NSW; ++j) wb[j] = p.wq + ((size_t)it.g * p.NT + tile_of(j)) * KB * kBlockBytes;
+
+    const int a_lane[2] = {m * 8 + (q ^ swz(m)), m * 8 + ((q + 4) ^ swz(m))};
+
+    auto body = [&](auto mcc) {
+        constexpr int C = decltype(mcc)::value;
+        // activation loads: wave w moves rows 4 C w .., eight rows a load.
+        // Past the end of a row whose K is not a multiple of 128 they take
+        // any 16 bytes of the row (the packed weights there are zero).
+        constexpr int NLA = C / 2;
+        const int8_t *asrc[NLA];
+        int achunk[NLA];
+#pragma unroll
+        for (int j = 0; j < NLA; ++j) {
+            const int r = 4 * C * wave + 8 * j + (l >> 3);
+            achunk[j] = 16 * ((l & 7) ^ swz(r));
+            asrc[j] = p.a + (size_t)max(srow[r], 0) * K;
+        }
+        auto dma_a = [&](int stage, int kg) {
+#pragma unroll
+            for (int j = 0; j < NLA; ++j)
+                dma16_untracked(asrc[j] + min(128 * kg + achunk[j], K - 16), &sA[stage * (TM * 8) + (4 * C * wave + 8 * j) * 8]);
+        };
+        v4i acc[C][NSW];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < NSW; ++j) acc[c][j] = v4i{0, 0, 0, 0};
+        u32x4 b0[NSW], b1[NSW], a0[C], a1[C];
+        auto boff = [&](int kb) { return (uint32_t)min(kb, KB - 1) * kBlockBytes + 16 * l; };
+        auto read_a = [&](u32x4(&av)[C], int stage, int h) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) av[c] = sA[stage * (TM * 8) + 128 * c + a_lane[h]];
+        };
+        dma_a(0, 0);
+        {
+            const uint32_t o0 = boff(0), o1 = boff(1);
+#pragma unroll
+            for (int j = 0; j < NSW; ++j) b0[j] = *(const u32x4 *)(wb[j] + o0);
+#pragma unroll
+            for (int j = 0; j < NSW; ++j) b1[j] = *(const u32x4 *)(wb[j] + o1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        dma_a(1, min(1, KG - 1));
+        read_a(a0, 0, 0);
+
+        // half a step: the m-tiles times one 64-wide k block; each subtile's
+        // operand is replaced by the one of two half steps later once its
+        // last matrix instruction is issued
+        auto half = [&](u32x4(&bv)[NSW], u32x4(&av)[C], int kb_next) {
+            const uint32_t o = boff(kb_next);
+#pragma unroll
+            for (int j = 0; j < NSW; ++j) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) mfma_acc(acc[c][j], bv[j], av[c]);
+                bv[j] = *(const u32x4 *)(wb[j] + o);
+            }
+        };
+        int s0 = 0, s1 = 1, s2 = 2;  // the stages of steps kg, kg + 1, kg + 2
+#pragma unroll 1
+        for (int kg = 0; kg < KG; ++kg) {
+            read_a(a1, s0, 1);
+            half(b0, a0, 2 * kg + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            // everything but the newest NSW weight loads has landed, this
+            // wave's activation loads of step kg + 1 among it; after the
+            // barrier every wave's have, and every wave is done with the
+            // stage that step kg + 2 takes
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(NSW));
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            dma_a(s2, min(kg + 2, KG - 1));
+            __builtin_amdgcn_sched_barrier(0);
+            read_a(a0, s1, 0);
+            half(b1, a1, 2 * kg + 3);
+            const int t = s0;
+            s0 = s1;
+            s1 = s2;
+            s2 = t;
+        }
+        mfma_drain();
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load into LDS outlives the block
+
+        // epilogue: lane (m, q) holds, of token 16 c + m, outputs 4 j' + i of
+        // the 16 at 64 st + 16 q of its subtiles (packed_row)
+        const int NC = ACT == MOE_ACT_SWIGLU ? p.N >> 1 : p.N;
+        constexpr int NO = ACT == MOE_ACT_SWIGLU ? HSW : NSW;
+        const int t0 = (it.nb * 4 + wave) * NO;  // the wave's first output subtile
+        const float *ws = p.ws + (size_t)it.g * p.N;
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+            const int n = packed_row(t0 + j, 4 * q);
+            if (n >= NC) continue;
+            float wsg[4], wsu[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wsg[i] = ws[n + i];
+                wsu[i] = ACT == MOE_ACT_SWIGLU ? ws[NC + n + i] : 0.0f;
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int r = 16 * c + m;
+                if (r >= it.mrows) continue;
+                const int src = srow[r];
+                const float sa = p.as[max(src, 0)];
+                float o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[i] = (float)acc[c][j][i] * sa * wsg[i];
+                    if (ACT == MOE_ACT_SWIGLU) o[i] = silu_mul(o[i], (float)acc[c][j + HSW][i] * sa * wsu[i]);
+                    if (src < 0) o[i] = 0.0f;  // a row without a source
+                }
+                *(uint2 *)(p.out + (size_t)(it.m0 + r) * NC + n) =
+                    make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+            }
+        }
+    };
+    if constexpr (MC == 8) {
+        if (mc > 6)
+            body(std::integral_constant<int, 8>());
+        else if (mc > 4)
+            body(std::integral_constant<int, 6>());
+        else if (mc > 2)
+            body(std::integral_constant<int, 4>());
+        else
+            body(std::integral_constant<int, 2>());
+    } else {
+        if (mc > 2)
+            body(std::integral_constant<int, 4>());
+        else
+            body(std::integral_constant<int, 2>());
+    }
+}
+
+template <int NSW, int MC>
+void launch(int act, Args a, hipStream_t st) {
+    constexpr int TM = 16 * MC;
+    a.NB = (a.NT + 4 * NSW - 1) / (4 * NSW);
+    const int64_t tiles = a.offsets ? (int64_t)a.R / TM + (a.R < a.G ? a.R : a.G) : (a.R + TM - 1) / TM;
+    const dim3 grid((unsigned)((tiles * a.NB + 7) / 8 * 8));  // a whole slice per XCD
+    if (act == MOE_ACT_SWIGLU)
+        hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_SWIGLU, NSW, MC>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_NONE, NSW, MC>), grid, dim3(256), 0, st, a);
+}
+
+}  // namespace
+
+void launch_tiled(int act, Args a, hipStream_t st) {
+    launch<8, 8>(act, a, st);
+}
+
+}  // namespace w8
+}  // namespace moe

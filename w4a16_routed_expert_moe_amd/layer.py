@@ -9,7 +9,9 @@ call, which keeps y in fp32 and never stores it; a single token takes the
 whole layer in one call, moe_w4a16_decode_token, where the device supports
 its shape).  Experts in FP4 (``ExpertWeights.fmt == "fp4"``, the release's
 own expert format) take moe_mxfp4_decode_token for a single token and
-otherwise moe_mxfp4_grouped_gemm for both GEMMs and the separate combine.  Buffers are allocated once per token count and reused,
+otherwise moe_mxfp4_grouped_gemm for both GEMMs and the separate combine;
+experts in INT8 (fmt "int8", one scale per output channel) take moe_w8a8_experts
+after the routing.  Buffers are allocated once per token count and reused,
 so the sequence can be captured in a HIP graph.
 """
 from __future__ import annotations
@@ -31,6 +33,7 @@ class ExpertWeights:
          G*2I*H/2 bytes; s13: fp16 [G][2I][H/128].
     w2:  INT4 codes of the down projection, G*H*I/2 bytes; s2: fp16 [G][H][I/128].
     fmt "fp4": E2M1 codes in the FP4 layout, s13 UE8M0 [G][2I][H/32], s2 UE8M0 [G][H][I/32].
+    fmt "int8": int8 codes in the layout of moe_w8a8_prepack, s13 fp32 [G][2I], s2 fp32 [G][H].
     """
     w13: torch.Tensor
     s13: torch.Tensor
@@ -45,7 +48,11 @@ class ExpertWeights:
 
 def prepack(canonical: torch.Tensor, n_groups: int, N: int, K: int, stream=None,
             fmt: str = "int4") -> torch.Tensor:
-    """Canonical codes (device, uint8) -> the streamed layout (a new tensor)."""
+    """Canonical codes (device, uint8; int8 for ``fmt`` "int8") -> the streamed layout (a new tensor)."""
+    if fmt == "int8":
+        out = torch.empty(L.moe_w8a8_packed_bytes(n_groups, N, K), dtype=torch.int8, device=canonical.device)
+        L.moe_w8a8_prepack(n_groups, N, K, canonical.reshape(-1), out, stream)
+        return out
     out = torch.empty(n_groups * N * K // 2, dtype=torch.uint8, device=canonical.device)
     fn = L.moe_w4a16_prepack if fmt == "int4" else L.moe_mxfp4_prepack
     fn(n_groups, N, K, canonical.reshape(-1), out, stream)
@@ -55,6 +62,11 @@ def prepack(canonical: torch.Tensor, n_groups: int, N: int, K: int, stream=None,
 def upload_weights(w13, s13, w2, s2, device="cuda", fmt: str = "int4") -> ExpertWeights:
     """Host canonical arrays (numpy, stacked over groups) -> resident ExpertWeights."""
     G, twoI = w13.shape[0], w13.shape[1]
+    if fmt == "int8":  # codes [G][2I][H] and [G][H][I] (one byte each), scales [G][2I] and [G][H]
+        H, I = w13.shape[2], twoI // 2
+        dev = [torch.from_numpy(a.copy()).to(device) for a in (w13, s13, w2, s2)]
+        return ExpertWeights(w13=prepack(dev[0], G, twoI, H, fmt=fmt), s13=dev[1].reshape(G, twoI),
+                             w2=prepack(dev[2], G, H, I, fmt=fmt), s2=dev[3].reshape(G, H), fmt=fmt)
     H = w13.shape[2] * 2
     I = twoI // 2
     gs = 128 if fmt == "int4" else 32  # elements per scale along K
@@ -67,6 +79,20 @@ def upload_weights(w13, s13, w2, s2, device="cuda", fmt: str = "int4") -> Expert
         s2=torch.from_numpy(s2.reshape(G, H, I // gs).copy()).to(device), fmt=fmt)
 
 
+def quantize_weights_int8(w13: torch.Tensor, w2: torch.Tensor) -> ExpertWeights:
+    """bf16 expert weights on the device, [G][2I][H] (gate rows, then up rows)
+    and [G][H][I] -> INT8 with one scale per output channel
+    (moe_act_quant_int8 on the weight rows), in the streamed layout."""
+    out = []
+    for w in (w13, w2):
+        G, N, K = w.shape
+        codes = torch.empty((G, N, K), dtype=torch.int8, device=w.device)
+        scales = torch.empty((G, N), dtype=torch.float32, device=w.device)
+        L.moe_act_quant_int8(G * N, K, w, codes, scales)
+        out += [prepack(codes, G, N, K, fmt="int8"), scales]
+    return ExpertWeights(w13=out[0], s13=out[1], w2=out[2], s2=out[3], fmt="int8")
+
+
 def generate_weights(seed: int, layer: int, G: int, H: int, I: int, device="cuda",
                      scratch: torch.Tensor | None = None, fmt: str = "int4") -> ExpertWeights:
     """Synthetic weights of one layer drawn on the device (counter-based
@@ -75,6 +101,8 @@ def generate_weights(seed: int, layer: int, G: int, H: int, I: int, device="cuda
     ``scratch`` (uint8, >= G*2I*H/2 bytes) may be passed to avoid a temporary."""
     if fmt == "fp4":
         return _generate_fp4(seed, layer, G, H, I, device, scratch)
+    if fmt == "int8":
+        raise ValueError("synthetic weights are generated in the formats int4 and fp4")
     n13 = G * 2 * I * H // 2
     n2 = G * H * I // 2
     if scratch is None or scratch.numel() < n13:
@@ -113,7 +141,8 @@ def _generate_fp4(seed, layer, G, H, I, device, scratch) -> ExpertWeights:
 class Buffers:
     """Device buffers of one forward pass at token count T."""
 
-    def __init__(self, desc: L.MoeLayerDesc, T: int, device="cuda", fp8: bool = False):
+    def __init__(self, desc: L.MoeLayerDesc, T: int, device="cuda", fp8: bool = False,
+                 int8: bool = False):
         H, I, E, k, ns = desc.hidden, desc.inter, desc.n_routed, desc.top_k, desc.n_shared
         G, R = desc.groups, desc.rows(T)
         self.T = T
@@ -163,6 +192,15 @@ class Buffers:
             self.xdq = torch.empty((T * n, H), dtype=torch.bfloat16, device=device)
             self.hdq = torch.empty((R * n, I), dtype=torch.bfloat16, device=device)
 
+        # int8 activations of the layer with INT8 experts: x and h as codes
+        # with one fp32 scale per token (row)
+        self.int8 = int8
+        if int8:
+            self.xq8 = torch.empty((T, H), dtype=torch.int8, device=device)
+            self.xqs8 = torch.empty(T, dtype=torch.float32, device=device)
+            self.hq8 = torch.empty((R, I), dtype=torch.int8, device=device)
+            self.hqs8 = torch.empty(R, dtype=torch.float32, device=device)
+
     def check_decode(self) -> None:
         """After the one-launch decode step: wait for the device, then raise
         ``DecodeTimeout`` if a wait of any call since the last check timed out
@@ -204,6 +242,15 @@ class MoELayer:
         d, T = self.desc, buf.T
         H, I = d.hidden, d.inter
         ex = self.experts
+        if ex.fmt == "int8":
+            if not buf.int8:
+                raise ValueError("the layer with INT8 experts needs Buffers(..., int8=True)")
+            L.moe_route_permute(d, T, x, self.w_router, self.gate_bias, buf.logits, buf.topk_idx, buf.topk_w,
+                                buf.group_offsets, buf.sorted_token, buf.row_of_slot, buf.ws, stream)
+            L.moe_w8a8_experts(d, T, x, buf.topk_w, buf.group_offsets, buf.sorted_token, buf.row_of_slot, ex.w13,
+                               ex.s13, ex.w2, ex.s2, buf.xq8, buf.xqs8, buf.h, buf.hq8, buf.hqs8, buf.y, buf.out,
+                               stream)
+            return buf.out
         if self.w4a8:
             # W4A8: x and h quantised to e4m3 per token per 128; from
             # MOE_TILED_MIN_TOKENS tokens both GEMMs on the block-scaled
