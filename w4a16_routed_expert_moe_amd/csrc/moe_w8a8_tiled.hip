@@ -3,11 +3,11 @@
 // the weight rows.
 //
 // Per 128-wide k step the tile's activation codes (128 bytes a row) go from
-// global memory straight into one of three LDS stages, a step and a half
+// global memory straight into one of four LDS stages, two and a half steps
 // ahead, and every wave reads all of them; the weights, which no two waves of
-// a workgroup share, go from global memory into registers, one to two half
-// steps (64 k) ahead, so that per matrix instruction of 16 cycles only
-// 1024 / NSW bytes come out of LDS.  The sums are exact in int32, so the k
+// a workgroup share, go from global memory into registers, four half steps
+// (64 k) ahead, so that per matrix instruction of 16 cycles only 1024 / NSW
+// bytes come out of LDS.  The sums are exact in int32, so the k
 // loop holds nothing but loads and matrix instructions; both scales are
 // applied in the epilogue.
 // The wave multiplies only the m-tiles (16 rows) that have rows: the count is
@@ -20,7 +20,7 @@ namespace moe {
 namespace w8 {
 namespace {
 
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 
 // Chunk c (16 bytes) of row r of a stage sits at chunk c ^ swz(r): the eight
 // rows of each parity that one 16-lane group of an operand read takes then
@@ -44,7 +44,10 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
     constexpr int TM = 16 * MC;  // times 64 NSW weight rows
     constexpr int HSW = NSW / 2;
     __shared__ u32x4 sA[kStages * TM * 8];
+    constexpr int NO = ACT == MOE_ACT_SWIGLU ? HSW : NSW;  // output subtiles per wave
+    constexpr int NWS = NSW / 4 > 0 ? NSW / 4 : 1;         // weight scales per thread
     __shared__ int srow[TM];
+    __shared__ float sas[TM], sws[256 * NWS];
     if constexpr (NSW * MC >= 64) asm volatile("" ::: "a0");
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id();
     const int m = l & 15, q = l >> 4;
@@ -64,6 +67,16 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
     }
     __syncthreads();
     const int mc = (it.mrows + 15) >> 4;  // m-tiles that have rows
+    // The epilogue's scales: one row scale and NWS weight scales per thread.
+    // Scale x of the tile belongs to output x % (64 NO) of the tile's columns
+    // (SwiGLU: first the gate columns', then the up columns').
+    const float my_as = tid < TM ? p.as[max(srow[tid], 0)] : 0.0f;
+    float my_ws[NWS];
+#pragma unroll
+    for (int i = 0; i < NWS; ++i) {
+        const int x = 256 * i + tid, col = min(it.nb * (64 * NO) + x % (64 * NO), (ACT == MOE_ACT_SWIGLU ? p.N >> 1 : p.N) - 1);
+        my_ws[i] = p.ws[(size_t)it.g * p.N + (ACT == MOE_ACT_SWIGLU && x >= 64 * NO ? p.N >> 1 : 0) + col];
+    }
 
     // the wave's subtiles: NSW consecutive ones, or (SwiGLU) NSW/2 of the
     // gate projection and the same of the up projection
@@ -102,29 +115,30 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int j = 0; j < NSW; ++j) acc[c][j] = v4i{0, 0, 0, 0};
-        u32x4 b0[NSW], b1[NSW], a0[C], a1[C];
+        u32x4 b[4][NSW], a0[C], a1[C];  // the weights of four half steps
         auto boff = [&](int kb) { return (uint32_t)min(kb, KB - 1) * kBlockBytes + 16 * l; };
         auto read_a = [&](u32x4(&av)[C], int stage, int h) {
 #pragma unroll
             for (int c = 0; c < C; ++c) av[c] = sA[stage * (TM * 8) + 128 * c + a_lane[h]];
         };
         dma_a(0, 0);
-        {
-            const uint32_t o0 = boff(0), o1 = boff(1);
+        dma_a(1, min(1, KG - 1));
+        dma_a(2, min(2, KG - 1));
 #pragma unroll
-            for (int j = 0; j < NSW; ++j) b0[j] = *(const u32x4 *)(wb[j] + o0);
+        for (int h = 0; h < 4; ++h) {
+            const uint32_t o = boff(h);
 #pragma unroll
-            for (int j = 0; j < NSW; ++j) b1[j] = *(const u32x4 *)(wb[j] + o1);
+            for (int j = 0; j < NSW; ++j) b[h][j] = *(const u32x4 *)(wb[j] + o);
         }
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        // the activation loads of steps 0 to 2 have landed, then every wave's
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(4 * NSW));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        dma_a(1, min(1, KG - 1));
         read_a(a0, 0, 0);
 
         // half a step: the m-tiles times one 64-wide k block; each subtile's
-        // operand is replaced by the one of two half steps later once its
+        // operand is replaced by the one of four half steps later once its
         // last matrix instruction is issued
         auto half = [&](u32x4(&bv)[NSW], u32x4(&av)[C], int kb_next) {
             const uint32_t o = boff(kb_next);
@@ -135,62 +149,78 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
                 bv[j] = *(const u32x4 *)(wb[j] + o);
             }
         };
-        int s0 = 0, s1 = 1, s2 = 2;  // the stages of steps kg, kg + 1, kg + 2
-#pragma unroll 1
-        for (int kg = 0; kg < KG; ++kg) {
+        int s0 = 0;  // the stage of step kg
+        auto step = [&](u32x4(&bl)[NSW], u32x4(&bh)[NSW], int kg) {
             read_a(a1, s0, 1);
-            half(b0, a0, 2 * kg + 2);
+            half(bl, a0, 2 * kg + 4);
             __builtin_amdgcn_sched_barrier(0);
-            // everything but the newest NSW weight loads has landed, this
-            // wave's activation loads of step kg + 1 among it; after the
-            // barrier every wave's have, and every wave is done with the
-            // stage that step kg + 2 takes
-            __builtin_amdgcn_s_waitcnt(vmcnt_imm(NSW));
+            // This wave's activation loads of step kg + 1 have landed: they
+            // are older than the weight loads of the last four half steps.
+            // After the barrier every wave's have, and every wave is done
+            // with the stage of step kg - 1, which step kg + 3 takes.
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(4 * NSW));
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            dma_a(s2, min(kg + 2, KG - 1));
+            dma_a((s0 + 3) & 3, min(kg + 3, KG - 1));
             __builtin_amdgcn_sched_barrier(0);
-            read_a(a0, s1, 0);
-            half(b1, a1, 2 * kg + 3);
-            const int t = s0;
-            s0 = s1;
-            s1 = s2;
-            s2 = t;
+            s0 = (s0 + 1) & 3;
+            read_a(a0, s0, 0);
+            half(bh, a1, 2 * kg + 5);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int kg = 0;
+#pragma unroll 1
+        for (; kg + 1 < KG; kg += 2) {
+            step(b[0], b[1], kg);
+            step(b[2], b[3], kg + 1);
         }
+        if (kg < KG) step(b[0], b[1], kg);
         mfma_drain();
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load into LDS outlives the block
 
-        // epilogue: lane (m, q) holds, of token 16 c + m, outputs 4 j' + i of
-        // the 16 at 64 st + 16 q of its subtiles (packed_row)
+        // epilogue: the scales, requested before the k loop, go through LDS;
+        // lane (m, q) holds, of token 16 c + m, the 16 outputs at 64 st + 16 q
+        // of each four subtiles (packed_row), four per subtile
+        if (tid < TM) sas[tid] = my_as;
+#pragma unroll
+        for (int i = 0; i < NWS; ++i) sws[256 * i + tid] = my_ws[i];
+        __syncthreads();
         const int NC = ACT == MOE_ACT_SWIGLU ? p.N >> 1 : p.N;
-        constexpr int NO = ACT == MOE_ACT_SWIGLU ? HSW : NSW;
         const int t0 = (it.nb * 4 + wave) * NO;  // the wave's first output subtile
-        const float *ws = p.ws + (size_t)it.g * p.N;
+        f32x4 wg[NO], wu[NO];
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-            const int n = packed_row(t0 + j, 4 * q);
-            if (n >= NC) continue;
-            float wsg[4], wsu[4];
+            wg[j] = *(const f32x4 *)&sws[packed_row(wave * NO + j, 4 * q)];
+            wu[j] = ACT == MOE_ACT_SWIGLU ? *(const f32x4 *)&sws[64 * NO + packed_row(wave * NO + j, 4 * q)] : f32x4{};
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                wsg[i] = ws[n + i];
-                wsu[i] = ACT == MOE_ACT_SWIGLU ? ws[NC + n + i] : 0.0f;
-            }
+        for (int c = 0; c < C; ++c) {
+            const int r = 16 * c + m;
+            const bool live = srow[r] >= 0;  // a row without a source is zero
+            const float sa = sas[r];
+            uint2 w[NO];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int r = 16 * c + m;
-                if (r >= it.mrows) continue;
-                const int src = srow[r];
-                const float sa = p.as[max(src, 0)];
+            for (int j = 0; j < NO; ++j) {
                 float o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    o[i] = (float)acc[c][j][i] * sa * wsg[i];
-                    if (ACT == MOE_ACT_SWIGLU) o[i] = silu_mul(o[i], (float)acc[c][j + HSW][i] * sa * wsu[i]);
-                    if (src < 0) o[i] = 0.0f;  // a row without a source
+                    o[i] = (float)acc[c][j][i] * sa * wg[j][i];
+                    if (ACT == MOE_ACT_SWIGLU) o[i] = silu_mul(o[i], (float)acc[c][j + HSW][i] * sa * wu[j][i]);
                 }
-                *(uint2 *)(p.out + (size_t)(it.m0 + r) * NC + n) =
-                    make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+                w[j] = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+                if (!live) w[j] = make_uint2(0u, 0u);
+            }
+            if (r >= it.mrows) continue;
+            uint16_t *row = p.out + (size_t)(it.m0 + r) * NC;
+            if constexpr (NO == 1) {
+                const int n = packed_row(t0, 4 * q);
+                if (n < NC) *(uint2 *)(row + n) = w[0];
+            } else {
+#pragma unroll
+                for (int j = 0; j < NO; j += 2) {
+                    const int n = packed_row(t0 + j, 4 * q);
+                    if (n < NC) *(u32x4 *)(row + n) = u32x4{w[j].x, w[j].y, w[j + 1].x, w[j + 1].y};
+                }
             }
         }
     };
