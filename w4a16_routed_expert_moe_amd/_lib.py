@@ -137,15 +137,19 @@ def _check(fn: str, status: int):
         raise MoeError(fn, status, lib().moe_status_str(status).decode())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+def _stream(stream) -> int:
+    if stream is None:  # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+    return int(stream)
 
 
 def _ptr(t, name, dtype, numel, optional=False):
+    # the common case first: a call checks up to 17 tensors, and a decode
+    # step's calls are bound by the host
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
     if t is None:
         if optional:
             return None
@@ -156,9 +160,7 @@ def _ptr(t, name, dtype, numel, optional=False):
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if t.numel() < numel:
-        raise ValueError("%s holds %d elements, needs %d" % (name, t.numel(), numel))
-    return ctypes.c_void_p(t.data_ptr())
+    raise ValueError("%s holds %d elements, needs %d" % (name, t.numel(), numel))
 
 
 # ------------------------------------------------------------------ entry points
@@ -442,6 +444,11 @@ def moe_w8a8_packed_bytes(n_groups: int, N: int, K: int) -> int:
     return int(lib().moe_w8a8_packed_bytes(n_groups, N, K))
 
 
+def _packed(n_groups: int, N: int, K: int) -> int:
+    """moe_w8a8_packed_bytes of valid sizes, without the call (the entry points refuse the others)."""
+    return n_groups * ((N + 63) & -64) * ((K + 127) & -128)
+
+
 def moe_w8a8_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stream=None):
     _check("moe_w8a8_prepack", lib().moe_w8a8_prepack(
         n_groups, N, K, _ptr(w_canonical, "w_canonical", torch.int8, n_groups * N * K),
@@ -451,7 +458,7 @@ def moe_w8a8_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, strea
 def moe_w8a8_gemm(M: int, N: int, K: int, a, a_scales, w_packed, w_scales, out, stream=None):
     _check("moe_w8a8_gemm", lib().moe_w8a8_gemm(
         M, N, K, _ptr(a, "a", torch.int8, M * K), _ptr(a_scales, "a_scales", torch.float32, M),
-        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(1, N, K)),
+        _ptr(w_packed, "w_packed", torch.int8, _packed(1, N, K)),
         _ptr(w_scales, "w_scales", torch.float32, N), _ptr(out, "out", torch.bfloat16, M * N), _stream(stream)))
 
 
@@ -459,7 +466,7 @@ def moe_w8a8_linear(M: int, N: int, K: int, x, w_packed, w_scales, codes, scales
     """moe_act_quant_int8 + moe_w8a8_gemm in one call; codes and scales are scratch."""
     _check("moe_w8a8_linear", lib().moe_w8a8_linear(
         M, N, K, _ptr(x, "x", torch.bfloat16, M * K),
-        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(1, N, K)),
+        _ptr(w_packed, "w_packed", torch.int8, _packed(1, N, K)),
         _ptr(w_scales, "w_scales", torch.float32, N), _ptr(codes, "codes", torch.int8, M * K),
         _ptr(scales, "scales", torch.float32, M), _ptr(out, "out", torch.bfloat16, M * N), _stream(stream)))
 
@@ -473,7 +480,7 @@ def moe_w8a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_s
         ctypes.byref(desc), T, _ptr(a, "a", torch.int8, a_rows * K),
         _ptr(a_scales, "a_scales", torch.float32, a_rows),
         _ptr(a_gather, "a_gather", torch.int32, R, optional=True), n_src, N, K,
-        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(G, N, K)),
+        _ptr(w_packed, "w_packed", torch.int8, _packed(G, N, K)),
         _ptr(w_scales, "w_scales", torch.float32, G * N),
         _ptr(group_offsets, "group_offsets", torch.int32, G + 1), act,
         _ptr(out, "out", torch.bfloat16, R * out_cols), _stream(stream)))
@@ -488,9 +495,9 @@ def moe_w8a8_experts(desc: MoeLayerDesc, T: int, x, topk_w, group_offsets, sorte
         _ptr(topk_w, "topk_w", torch.float32, T * desc.top_k),
         _ptr(group_offsets, "group_offsets", torch.int32, G + 1),
         _ptr(sorted_token, "sorted_token", torch.int32, R), _ptr(row_of_slot, "row_of_slot", torch.int32, T * S),
-        _ptr(w13_packed, "w13_packed", torch.int8, moe_w8a8_packed_bytes(G, 2 * I, H)),
+        _ptr(w13_packed, "w13_packed", torch.int8, _packed(G, 2 * I, H)),
         _ptr(w13_scales, "w13_scales", torch.float32, G * 2 * I),
-        _ptr(w2_packed, "w2_packed", torch.int8, moe_w8a8_packed_bytes(G, H, I)),
+        _ptr(w2_packed, "w2_packed", torch.int8, _packed(G, H, I)),
         _ptr(w2_scales, "w2_scales", torch.float32, G * H), _ptr(xq, "xq", torch.int8, T * H),
         _ptr(xqs, "xqs", torch.float32, T), _ptr(h, "h", torch.bfloat16, R * I),
         _ptr(hq, "hq", torch.int8, R * I), _ptr(hqs, "hqs", torch.float32, R),

@@ -39,6 +39,7 @@ struct Args {
     uint16_t *out;           // bf16 [R][N] or [R][N/2] (SwiGLU)
     int KB, NT;              // 64-wide k blocks and 16-row subtiles per group in the packed weights
     int NB;                  // n-blocks (the instance's tile width)
+    int qrows;               // fused quantisation: rows of a tile
 };
 
 __device__ __forceinline__ v4i mfma_i8(u32x4 a, u32x4 b, v4i c) {

@@ -10,6 +10,7 @@
 // |a| <= 127 and |w| <= 128, so the sum stays below 2^31 up to K = 65536 and
 // its order does not matter: every kernel and every split of K gives the same
 // bits.
+#include "moe_route_common.h"
 #include "moe_w8a8.h"
 
 namespace moe {
@@ -109,32 +110,37 @@ __global__ void k_w8a8_prepack(const int8_t *__restrict__ src, int8_t *__restric
 // ---------------------------------------------------------------- weight stream
 // Few rows per group: the weights' bytes are the bound.  A workgroup of W
 // waves takes NS subtiles (16 weight rows each; SwiGLU: NS/2 of the gate and
-// the same NS/2 of the up projection) and at most 16 C rows of one group;
-// the waves split K: wave w takes k blocks w, w + W, ..., every weight byte
+// the same NS/2 of the up projection) and at most 16 rows of one group; the
+// waves split K: wave w takes k blocks w, w + W, ..., every weight byte
 // goes straight from HBM into the registers of the one wave that multiplies
 // it, U blocks ahead, and the waves' int32 partial sums meet in LDS.
-// Q (C = 1, K <= 64 W U): the rows come in bf16 and are quantised here, each
-// workgroup its own copy (a row is 2K bytes, in L2), while the weights are
-// in flight: one launch less.
-template <int ACT, int NS, int C, int W, int U, bool Q>
+// Q (K <= kFusedMaxK): the rows come in bf16 and every workgroup
+// quantises its own copy of them into LDS while its weights are in flight (a
+// row is 2K bytes, in L2): one launch less.
+constexpr int kFusedMaxK = 4096;  // 8 elements per thread of 8 waves
+
+template <int ACT, int NS, int W, int U, bool Q>
 __global__ __launch_bounds__(64 * W) void k_w8a8_stream(Args p) {
-    static_assert(!Q || C == 1, "the fused quantisation takes one m-tile");
-    __shared__ int sred[W * NS * C * 256];
-    __shared__ int srow[16 * C];
-    __shared__ uint32_t smax[Q ? 16 * W : 1];
-    __shared__ float sscale[16];  // Q: the rows' scales
+    static_assert(!Q || W == 8, "the fused quantisation gives each thread 8 of 4096 elements");
+    constexpr int RB = 4;  // rows quantised at a time
+    __shared__ int sred[W * NS * 256];
+    __shared__ int srow[16];
+    __shared__ float sscale[16];
+    __shared__ uint32_t smax[Q ? RB * W : 1];
+    extern __shared__ __attribute__((aligned(16))) int8_t sq[];  // Q: codes [rows][K + 16]
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id();
     const int m = l & 15, q = l >> 4;
     TileItem it;
+    const int TM = Q ? p.qrows : 16;  // rows of a tile (Q: as many as the launch gave LDS for)
     if (p.offsets) {
-        if (!workgroup_tile_item(p.NB, 16 * C, p.offsets, p.G, p.R, it)) return;
+        if (!workgroup_tile_item(p.NB, TM, p.offsets, p.G, p.R, it)) return;
     } else {  // one group: the blocks in order, the m-tiles of an n-block side by side
-        const int mt = (p.R + 16 * C - 1) / (16 * C);
+        const int mt = (p.R + TM - 1) / TM;
         it.g = 0;
         it.nb = blockIdx.x / mt;
-        it.m0 = (blockIdx.x - it.nb * mt) * 16 * C;
+        it.m0 = (blockIdx.x - it.nb * mt) * TM;
         if (it.nb >= p.NB) return;
-        it.mrows = min(16 * C, p.R - it.m0);
+        it.mrows = min(TM, p.R - it.m0);
     }
     const int K = p.K, KB = p.KB, NTH = p.NT >> 1;
     // subtile j of the workgroup
@@ -150,121 +156,115 @@ __global__ __launch_bounds__(64 * W) void k_w8a8_stream(Args p) {
     auto load_b = [&](int kb0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t off = (uint32_t)min(kb0 + u * W + wave, KB - 1) * kBlockBytes + 16 * l;
+            if (kb0 + u * W + wave < KB) {
+                const uint32_t off = (uint32_t)(kb0 + u * W + wave) * kBlockBytes + 16 * l;
 #pragma unroll
-            for (int j = 0; j < NS; ++j) b[u][j] = __builtin_nontemporal_load((const u32x4 *)(wb[j] + off));
+                for (int j = 0; j < NS; ++j) b[u][j] = __builtin_nontemporal_load((const u32x4 *)(wb[j] + off));
+            }
         }
     };
     load_b(0);
-    // the source row of row 16 c + m of the tile (-1: none)
-    int sr[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int r = 16 * c + m;
-        sr[c] = -1;
-        if (r < it.mrows) {
-            sr[c] = it.m0 + r;
+    // the source row of each row of the tile (-1: none) and its scale
+    if (tid < 16) {
+        int src = -1;
+        if (tid < it.mrows) {
+            src = it.m0 + tid;
             if (p.gather) {
-                const int t = p.gather[it.m0 + r];
-                sr[c] = (unsigned)t < (unsigned)p.n_src ? t : -1;
+                const int t = p.gather[it.m0 + tid];
+                src = (unsigned)t < (unsigned)p.n_src ? t : -1;
             }
         }
-        if (wave == 0 && q == 0) srow[r] = sr[c];
+        srow[tid] = src;
+        if (!Q) sscale[tid] = p.as[max(src, 0)];
     }
-    v4i acc[C][NS];
+    __syncthreads();
+    v4i acc[NS];
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int j = 0; j < NS; ++j) acc[c][j] = v4i{0, 0, 0, 0};
-    float rscale = 0.0f;  // Q: the scale of row m
+    for (int j = 0; j < NS; ++j) acc[j] = v4i{0, 0, 0, 0};
 
     if constexpr (Q) {
-        const uint16_t *xr = p.x + (size_t)max(sr[0], 0) * K;
-        u32x4 v[U][2];
-        uint32_t mx = 0u;
+        const int LD = K + 16;  // 16 bytes of padding: 16 rows at one k sit on distinct banks
+        const bool in = 8 * tid < K;
+        for (int r0 = 0; r0 < it.mrows; r0 += RB) {
+            u32x4 v[RB];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = 64 * (u * W + wave) + 16 * q;
-            const bool in = k < K && sr[0] >= 0;
-            v[u][0] = v[u][1] = u32x4{0u, 0u, 0u, 0u};
-            if (in) {
-                v[u][0] = *(const u32x4 *)(xr + k);
-                v[u][1] = *(const u32x4 *)(xr + k + 8);
+            for (int i = 0; i < RB; ++i) {
+                v[i] = u32x4{0u, 0u, 0u, 0u};
+                const int src = r0 + i < it.mrows ? __builtin_amdgcn_readfirstlane(srow[r0 + i]) : -1;
+                if (in && src >= 0) v[i] = *(const u32x4 *)(p.x + (size_t)src * K + 8 * tid);
             }
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                if (r0 + i < it.mrows) {
+                    uint32_t mx = pk_max_abs(pk_max_abs(pk_max_abs(pk_max_abs(0u, v[i][0]), v[i][1]), v[i][2]), v[i][3]);
+                    mx = route::wave_max32(max(mx & 0xFFFFu, mx >> 16));
+                    if (l == 0) smax[i * W + wave] = mx;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < RB; ++i) {
+                if (r0 + i < it.mrows) {
+                    uint32_t mx = 0u;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) mx = max(mx, smax[i * W + w]);
+                    const RowScale s = row_scale(mx);
+                    if (tid == 0) sscale[r0 + i] = s.scale;
+                    if (in) *(uint2 *)(sq + (size_t)(r0 + i) * LD + 8 * tid) = quant8(v[i], s);
+                }
+            }
+            __syncthreads();
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx = pk_max_abs(pk_max_abs(mx, v[u][0][i]), v[u][1][i]);
-        mx = max(mx & 0xFFFFu, mx >> 16);
-        mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, kWave));
-        mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, kWave));
-        if (q == 0) smax[16 * wave + m] = mx;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < W; ++w) mx = max(mx, smax[16 * w + m]);
-        const RowScale s = row_scale(mx);
-        rscale = s.scale;
+        const int8_t *ar = sq + (size_t)min(m, it.mrows - 1) * LD + 16 * q;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (u * W + wave >= KB) break;
-            const uint2 lo = quant8(v[u][0], s), hi = quant8(v[u][1], s);
-            const u32x4 av = u32x4{lo.x, lo.y, hi.x, hi.y};
+            const int kb = u * W + wave;
+            if (kb < KB) {
+                // past the end of a row: any of its bytes, the weights there are zero
+                const u32x4 av = *(const u32x4 *)(ar + min(64 * kb, K - 16 - 16 * q));
 #pragma unroll
-            for (int j = 0; j < NS; ++j) acc[0][j] = mfma_i8(b[u][j], av, acc[0][j]);
+                for (int j = 0; j < NS; ++j) acc[j] = mfma_i8(b[u][j], av, acc[j]);
+            }
         }
     } else {
-        const int8_t *ar[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c) ar[c] = p.a + (size_t)max(sr[c], 0) * K;
+        const int8_t *ar = p.a + (size_t)max(srow[m], 0) * K;
         for (int kb0 = 0;;) {
-            u32x4 av[U][C];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                // past the end of a row whose K is not a multiple of 128: any
-                // 16 bytes of the row, the packed weights there are zero
-                const int k = min(64 * (kb0 + u * W + wave) + 16 * q, K - 16);
-#pragma unroll
-                for (int c = 0; c < C; ++c) av[u][c] = *(const u32x4 *)(ar[c] + k);
-            }
+            u32x4 av[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (kb0 + u * W + wave < KB)
+                    av[u] = *(const u32x4 *)(ar + min(64 * (kb0 + u * W + wave) + 16 * q, K - 16));
 #pragma unroll
-                    for (int j = 0; j < NS; ++j)
+            for (int u = 0; u < U; ++u)
+                if (kb0 + u * W + wave < KB) {
 #pragma unroll
-                        for (int c = 0; c < C; ++c) acc[c][j] = mfma_i8(b[u][j], av[u][c], acc[c][j]);
+                    for (int j = 0; j < NS; ++j) acc[j] = mfma_i8(b[u][j], av[u], acc[j]);
+                }
             kb0 += U * W;
             if (kb0 >= KB) break;
             load_b(kb0);
         }
     }
-    // the waves' partial sums: [wave][j][c][i][lane]
+    // the waves' partial sums: [wave][j][lane][i]
 #pragma unroll
-    for (int j = 0; j < NS; ++j)
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            *(v4i *)&sred[((wave * NS + j) * C + c) * 256 + 4 * l] = acc[c][j];
-    if constexpr (Q) {
-        if (wave == 0 && q == 0) sscale[m] = rscale;
-    }
+    for (int j = 0; j < NS; ++j) *(v4i *)&sred[(wave * NS + j) * 256 + 4 * l] = acc[j];
     __syncthreads();
     constexpr int NO = ACT == MOE_ACT_SWIGLU ? NS / 2 : NS;  // output subtiles
-    for (int i = tid; i < NO * C * 64; i += 64 * W) {
-        const int ln = i & 63, jc = i >> 6, c = jc % C, j = jc / C;
-        const int mm = ln & 15, qq = ln >> 4, r = 16 * c + mm;
+    if (tid < NO * 64) {
+        const int j = tid >> 6, r = l & 15, qq = l >> 4;
+        if (r >= it.mrows) return;
         v4i s0 = v4i{0, 0, 0, 0}, s1 = v4i{0, 0, 0, 0};
+#pragma unroll
         for (int w = 0; w < W; ++w) {
-            s0 += *(const v4i *)&sred[((w * NS + j) * C + c) * 256 + 4 * ln];
-            if (ACT == MOE_ACT_SWIGLU) s1 += *(const v4i *)&sred[((w * NS + j + NS / 2) * C + c) * 256 + 4 * ln];
+            s0 += *(const v4i *)&sred[(w * NS + j) * 256 + 4 * l];
+            if (ACT == MOE_ACT_SWIGLU) s1 += *(const v4i *)&sred[(w * NS + j + NS / 2) * 256 + 4 * l];
         }
-        if (r >= it.mrows) continue;
         const int t = ACT == MOE_ACT_SWIGLU ? it.nb * (NS / 2) + j : it.nb * NS + j;
         const int n = packed_row(t, 4 * qq);
         const int NC = ACT == MOE_ACT_SWIGLU ? p.N >> 1 : p.N;
-        if (n >= NC) continue;
+        if (n >= NC) return;
         const int src = srow[r];
-        const float sa = Q ? sscale[mm] : p.as[max(src, 0)];
+        const float sa = sscale[r];
         const float *ws = p.ws + (size_t)it.g * p.N + n;
         float o[4];
 #pragma unroll
@@ -277,36 +277,55 @@ __global__ __launch_bounds__(64 * W) void k_w8a8_stream(Args p) {
     }
 }
 
-template <int ACT, int NS, int C, bool Q>
-void launch_stream(Args a, hipStream_t st) {
-    constexpr int W = 8, U = 8;
+template <int ACT, int NS, int U, bool Q>
+void launch_stream_u(Args a, int rows, hipStream_t st) {
+    constexpr int W = 8;
     a.NB = (ACT == MOE_ACT_SWIGLU ? a.NT / 2 : a.NT) / (ACT == MOE_ACT_SWIGLU ? NS / 2 : NS);
-    const int64_t tiles = a.offsets ? (int64_t)a.R / (16 * C) + (a.R < a.G ? a.R : a.G) : (a.R + 16 * C - 1) / (16 * C);
+    const int TM = Q ? rows : 16;
+    a.qrows = rows;
+    int64_t tiles = a.offsets ? (int64_t)a.R / TM + (a.R < a.G ? a.R : a.G) : (a.R + TM - 1) / TM;
+    if (tiles > a.R) tiles = a.R;  // every tile has a row
     const dim3 grid((unsigned)((tiles * a.NB + 7) / 8 * 8));
-    hipLaunchKernelGGL((k_w8a8_stream<ACT, NS, C, W, U, Q>), grid, dim3(64 * W), 0, st, a);
+    const size_t lds = Q ? (size_t)rows * (a.K + 16) : 0;
+    hipLaunchKernelGGL((k_w8a8_stream<ACT, NS, W, U, Q>), grid, dim3(64 * W), lds, st, a);
 }
 
-constexpr int kFusedRows = 16;     // rows of one m-tile
-constexpr int kFusedMaxK = 4096;   // 64 W U
-constexpr int kStreamRows = 64;
+// U: the k blocks that each wave has in flight, as many as K gives it (up to 8)
+template <int ACT, int NS, bool Q>
+void launch_stream(const Args &a, int rows, hipStream_t st) {
+    if (a.KB <= 16)
+        launch_stream_u<ACT, NS, 2, Q>(a, rows, st);
+    else if (a.KB <= 32)
+        launch_stream_u<ACT, NS, 4, Q>(a, rows, st);
+    else
+        launch_stream_u<ACT, NS, 8, Q>(a, rows, st);
+}
+
+// Rows that a workgroup quantises for itself instead of a launch before (a
+// 4096 x 4096 projection: 5.9 against 8.5 us at 1 row, 6.8 against 8.5 at 4,
+// 9.3 against 8.8 at 8; the layer's experts at hidden 4096: 46 against 49 us
+// at 1 token, 128 against 131 at 4, 226 against 207 at 8).
+constexpr int kFusedRows = 4;
+// Rows up to which the weight stream is the faster kernel.  Dense, 4096 x
+// 4096: 6.2 against 9.5 us at 16 rows.  Grouped: the tiled kernel needs no
+// more bytes and has more of them in flight (the layer's experts: 207 against
+// 220 us at 8 tokens, 354 against 380 at 16).
+constexpr int kStreamRows = 16, kStreamRowsGrouped = 4;
 
 // rows: an upper bound of the rows of one group
 void launch_gemm(int act, const Args &a, int rows, hipStream_t st) {
+    const bool swiglu = act == MOE_ACT_SWIGLU;
+    // two subtiles per workgroup, or one where two would leave CUs without
+    // work (4096 columns: 5.5 against 6.2 us; 8192: 4.8 against 4.7)
+    const bool one = !swiglu && !a.offsets && a.NT <= 256;
     if (a.x) {
-        if (act == MOE_ACT_SWIGLU)
-            launch_stream<MOE_ACT_SWIGLU, 2, 1, true>(a, st);
-        else
-            launch_stream<MOE_ACT_NONE, 2, 1, true>(a, st);
-    } else if (rows <= 16) {
-        if (act == MOE_ACT_SWIGLU)
-            launch_stream<MOE_ACT_SWIGLU, 2, 1, false>(a, st);
-        else
-            launch_stream<MOE_ACT_NONE, 2, 1, false>(a, st);
-    } else if (rows <= kStreamRows) {
-        if (act == MOE_ACT_SWIGLU)
-            launch_stream<MOE_ACT_SWIGLU, 2, 4, false>(a, st);
-        else
-            launch_stream<MOE_ACT_NONE, 2, 4, false>(a, st);
+        swiglu ? launch_stream<MOE_ACT_SWIGLU, 2, true>(a, rows, st)
+        : one  ? launch_stream<MOE_ACT_NONE, 1, true>(a, rows, st)
+               : launch_stream<MOE_ACT_NONE, 2, true>(a, rows, st);
+    } else if (rows <= (a.offsets ? kStreamRowsGrouped : kStreamRows)) {
+        swiglu ? launch_stream<MOE_ACT_SWIGLU, 2, false>(a, rows, st)
+        : one  ? launch_stream<MOE_ACT_NONE, 1, false>(a, rows, st)
+               : launch_stream<MOE_ACT_NONE, 2, false>(a, rows, st);
     } else {
         launch_tiled(act, a, st);
     }

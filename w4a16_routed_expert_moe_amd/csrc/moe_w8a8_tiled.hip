@@ -39,8 +39,23 @@ __device__ __forceinline__ void mfma_acc(v4i &acc, u32x4 a, u32x4 b) {
 }
 __device__ __forceinline__ void mfma_drain() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-template <int ACT, int NSW, int MC>
-__global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
+// The work item of this workgroup in a dense product: find_tile_item's list
+// (m-tiles in chunks of four, n-block-major inside a chunk; a contiguous
+// slice per XCD) for one group, without its search.
+__device__ __forceinline__ bool dense_item(int NB, int TM, int R, TileItem &it) {
+    const int mt = (R + TM - 1) / TM, total = mt * NB, per = (total + 7) >> 3;
+    const int item = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || item >= total) return false;
+    const int ch = item / (4 * NB), rem = item - ch * 4 * NB, mc = min(4, mt - 4 * ch);
+    it.g = 0;
+    it.nb = rem / mc;
+    it.m0 = (4 * ch + rem - it.nb * mc) * TM;
+    it.mrows = min(TM, R - it.m0);
+    return true;
+}
+
+template <int ACT, int NSW, int MC, int PF, int OCC>
+__global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
     constexpr int TM = 16 * MC;  // times 64 NSW weight rows
     constexpr int HSW = NSW / 2;
     __shared__ u32x4 sA[kStages * TM * 8];
@@ -52,7 +67,7 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id();
     const int m = l & 15, q = l >> 4;
     TileItem it;
-    if (!workgroup_tile_item(p.NB, TM, p.offsets, p.G, p.R, it)) return;
+    if (p.offsets ? !workgroup_tile_item(p.NB, TM, p.offsets, p.G, p.R, it) : !dense_item(p.NB, TM, p.R, it)) return;
     const int K = p.K, KB = p.KB, KG = KB >> 1, NTH = p.NT >> 1;
     if (tid < TM) {
         int sr = -1;
@@ -115,7 +130,7 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int j = 0; j < NSW; ++j) acc[c][j] = v4i{0, 0, 0, 0};
-        u32x4 b[4][NSW], a0[C], a1[C];  // the weights of four half steps
+        u32x4 b[PF][NSW], a0[C], a1[C];  // the weights of PF half steps
         auto boff = [&](int kb) { return (uint32_t)min(kb, KB - 1) * kBlockBytes + 16 * l; };
         auto read_a = [&](u32x4(&av)[C], int stage, int h) {
 #pragma unroll
@@ -125,20 +140,20 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
         dma_a(1, min(1, KG - 1));
         dma_a(2, min(2, KG - 1));
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < PF; ++h) {
             const uint32_t o = boff(h);
 #pragma unroll
             for (int j = 0; j < NSW; ++j) b[h][j] = *(const u32x4 *)(wb[j] + o);
         }
         __builtin_amdgcn_sched_barrier(0);
         // the activation loads of steps 0 to 2 have landed, then every wave's
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(4 * NSW));
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(PF * NSW));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         read_a(a0, 0, 0);
 
         // half a step: the m-tiles times one 64-wide k block; each subtile's
-        // operand is replaced by the one of four half steps later once its
+        // operand is replaced by the one of PF half steps later once its
         // last matrix instruction is issued
         auto half = [&](u32x4(&bv)[NSW], u32x4(&av)[C], int kb_next) {
             const uint32_t o = boff(kb_next);
@@ -152,7 +167,7 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
         int s0 = 0;  // the stage of step kg
         auto step = [&](u32x4(&bl)[NSW], u32x4(&bh)[NSW], int kg) {
             read_a(a1, s0, 1);
-            half(bl, a0, 2 * kg + 4);
+            half(bl, a0, 2 * kg + PF);
             __builtin_amdgcn_sched_barrier(0);
             // This wave's activation loads of step kg + 1 have landed: they
             // are older than the weight loads of the last four half steps.
@@ -165,14 +180,14 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
             __builtin_amdgcn_sched_barrier(0);
             s0 = (s0 + 1) & 3;
             read_a(a0, s0, 0);
-            half(bh, a1, 2 * kg + 5);
+            half(bh, a1, 2 * kg + PF + 1);
             __builtin_amdgcn_sched_barrier(0);
         };
         int kg = 0;
 #pragma unroll 1
         for (; kg + 1 < KG; kg += 2) {
             step(b[0], b[1], kg);
-            step(b[2], b[3], kg + 1);
+            step(b[PF - 2], b[PF - 1], kg + 1);
         }
         if (kg < KG) step(b[0], b[1], kg);
         mfma_drain();
@@ -224,7 +239,9 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
             }
         }
     };
-    if constexpr (MC == 8) {
+    if constexpr (MC == 2) {
+        body(std::integral_constant<int, 2>());
+    } else if constexpr (MC == 8) {
         if (mc > 6)
             body(std::integral_constant<int, 8>());
         else if (mc > 4)
@@ -241,22 +258,49 @@ __global__ __launch_bounds__(256) void k_w8a8_tiled(Args p) {
     }
 }
 
-template <int NSW, int MC>
+template <int NSW, int MC, int PF, int OCC>
 void launch(int act, Args a, hipStream_t st) {
     constexpr int TM = 16 * MC;
     a.NB = (a.NT + 4 * NSW - 1) / (4 * NSW);
-    const int64_t tiles = a.offsets ? (int64_t)a.R / TM + (a.R < a.G ? a.R : a.G) : (a.R + TM - 1) / TM;
+    int64_t tiles = a.offsets ? (int64_t)a.R / TM + (a.R < a.G ? a.R : a.G) : (a.R + TM - 1) / TM;
+    if (tiles > a.R) tiles = a.R;  // every tile has a row
     const dim3 grid((unsigned)((tiles * a.NB + 7) / 8 * 8));  // a whole slice per XCD
     if (act == MOE_ACT_SWIGLU)
-        hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_SWIGLU, NSW, MC>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_SWIGLU, NSW, MC, PF, OCC>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_NONE, NSW, MC>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_NONE, NSW, MC, PF, OCC>), grid, dim3(256), 0, st, a);
 }
 
 }  // namespace
 
+// Which tile: the largest that leaves few CUs without a workgroup, for a
+// larger tile reads fewer bytes per product.  Dense, us (N = K = 4096; tiles
+// of rows x weight rows):
+//   rows       128 x 256   64 x 256   64 x 128   32 x 128
+//   61              18.1       16.7       12.2        9.8
+//   256             28.5       17.0       12.8       10.6
+//   512             29.0       17.9       13.9       17.7
+//   1024            30.0       21.7       22.6       31.6
+//   2048            36.9       40.5       46.9       61.6
+//   8192             119        149        169        246
+// Groups of few rows are bound by the weights' bytes: 64 x 128 tiles keep the
+// most of them in flight (the layer's experts at hidden 4096, 256 experts, 6
+// per token: 1162 us against 1177 with 128 x 256 at 1024 tokens, 1279 against
+// 1249 at 2048, where a group has 48 rows).
 void launch_tiled(int act, Args a, hipStream_t st) {
-    launch<8, 8>(act, a, st);
+    auto fills = [&](int TM, int TN) {
+        const int64_t tiles = (a.R + TM - 1) / TM + (a.offsets ? (a.R < a.G ? a.R : a.G) / 2 : 0);
+        return tiles * ((16 * a.NT + TN - 1) / TN) >= 160;
+    };
+    const bool few = a.offsets && a.R < 48 * (int64_t)a.G;
+    if (!few && fills(128, 256))
+        launch<4, 8, 2, 2>(act, a, st);
+    else if (!few && fills(64, 256))
+        launch<4, 4, 4, 2>(act, a, st);
+    else if (fills(64, 128))
+        launch<2, 4, 4, 3>(act, a, st);
+    else
+        launch<2, 2, 4, 4>(act, a, st);
 }
 
 }  // namespace w8
