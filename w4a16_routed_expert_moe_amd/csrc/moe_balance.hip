@@ -19,10 +19,15 @@ constexpr int kSlots = 4;          // experts per lane: E <= 256
 constexpr int kMaxExperts = kSlots * kWave;
 constexpr int kOneTokens = 128;    // up to here the loss is one workgroup's work, one launch
 constexpr int kOneSeqs = 64;
-constexpr int kMaxChunks = 512;    // token chunks of the partial sums
+constexpr int kChunks = 256;       // token chunks of the partial sums: one per CU ...
+constexpr int kMinChunk = 8, kMaxChunk = 128;  // ... of at least 8 tokens and at most as many as fit the registers
 
-// the tokens of one chunk: at most kMaxChunks of them (two per CU), 32 tokens at least
-int chunk_tokens(int T) { return T <= 32 * kMaxChunks ? 32 : (T + kMaxChunks - 1) / kMaxChunks; }
+// the tokens of one chunk, a power of two
+int chunk_tokens(int T) {
+    int C = kMinChunk;
+    while (C < kMaxChunk && (int64_t)C * kChunks * (T > 16384 ? 2 : 1) < T) C *= 2;
+    return C;
+}
 int chunk_count(int T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
 
 // Sigmoid s and its slope s (1 - s) from e = exp(-|x|), which neither
@@ -34,10 +39,8 @@ __device__ __forceinline__ float score(float x, float &slope) {
     slope = e * r * r;
     return x < 0.0f ? e * r : r;
 }
-__device__ __forceinline__ float score(float x) {
-    float slope;
-    return score(x, slope);
-}
+// the score alone (exp(-x) = inf gives 0)
+__device__ __forceinline__ float score(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 // the expert of slot i of a lane: VEC four consecutive ones (16-byte loads),
 // else one in each block of 64 (any E, any alignment)
@@ -128,94 +131,132 @@ Parts parts_of(void *ws, int chunks, int n, int E) {
 }
 
 // ---------------------------------------------------------------- loss
-// Tokens [a, b) of one sequence: the workgroup's sums over its live tokens.
-// On return thread e < E has the expert's probability sum and count, every
-// thread the number of live tokens.  Fixed order: wave w adds tokens a + w,
-// a + w + W, ..., then the waves are added in order.
-template <bool VEC, int W>
+// A workgroup of W waves holds the probabilities of its W U tokens in
+// registers (wave w those of tokens t0 + w, t0 + w + W, ...) and, each
+// thread, NI of their choices; then it goes through the segments, the parts of
+// sequences that lie among them.  A segment's sums: each wave adds its tokens
+// that belong to it, the waves meet in LDS and are added in order.  Two LDS
+// buffers in turn: one barrier per segment.
+template <int W>
 struct SegmentLds {
-    float red[W][kMaxExperts];
-    int32_t hist[kMaxExperts];
-    int32_t live[W];
+    float red[2][W][kMaxExperts];
+    int32_t hist[2][kMaxExperts];
+    int32_t live[2][W];
 };
-template <bool VEC, int W>
-__device__ __forceinline__ void segment_sums(const Seqs &q, const float *__restrict__ logits,
-                                             const int32_t *__restrict__ idx, int E, int k, int a, int b,
-                                             SegmentLds<VEC, W> &sh, float &prob, int &cnt, int &live) {
-    constexpr int U = 4;  // tokens in flight per wave
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    for (int e = tid; e < kMaxExperts; e += 64 * W) sh.hist[e] = 0;
-    __syncthreads();
-    float acc[kSlots] = {0.f, 0.f, 0.f, 0.f};
-    int n = 0;
-    for (int t0 = a + wave; t0 < b; t0 += U * W) {
+template <bool VEC, int W, int U>
+struct Tokens {
+    static constexpr int NI = (W * U * 8 + 64 * W - 1) / (64 * W);  // choices per thread (k <= 8)
+    float p[U][kSlots];
+    bool on[U];
+    int e[NI], te[NI];  // choice, its token
+
+    __device__ __forceinline__ void load(const Seqs &q, const float *__restrict__ logits,
+                                         const int32_t *__restrict__ idx, int E, int k, int t0, int t1) {
+        const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         float x[U][kSlots];
-        bool on[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int t = t0 + u * W;
-            on[u] = t < b && token_live(q, t);
-            load_row<VEC>(logits + (size_t)min(t, b - 1) * E, E, x[u]);
+            const int t = t0 + wave + u * W;
+            on[u] = t < t1;
+            if (t < t1) {
+                on[u] = token_live(q, t);
+                load_row<VEC>(logits + (size_t)t * E, E, x[u]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int at = tid + 64 * W * i;
+            te[i] = t0 + at / k;
+            e[i] = -1;
+            if (te[i] < t1) {
+                e[i] = idx[(size_t)t0 * k + at];
+                if (!token_live(q, te[i]) || (unsigned)e[i] >= (unsigned)E) e[i] = -1;
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float s[kSlots], sum = 0.0f;
+            if (t0 + wave + u * W >= t1) continue;
+            float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
-                s[i] = expert_of<VEC>(i) < E ? score(x[u][i]) : 0.0f;
-                sum += s[i];
+                p[u][i] = expert_of<VEC>(i) < E ? score(x[u][i]) : 0.0f;
+                sum += p[u][i];
             }
             sum = route::wave_tree_sum(sum);
-            const float inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : sum == 0.0f ? 0.0f : sum;  // NaN stays
-            if (on[u]) {
-                ++n;
+            const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 #pragma unroll
-                for (int i = 0; i < kSlots; ++i) acc[i] += s[i] * inv;
-            }
+            for (int i = 0; i < kSlots; ++i) p[u][i] *= inv;
         }
     }
+    // The sums over tokens [a, b): on return thread e < E has expert e's, and
+    // every thread below 64 * 4 the number of live tokens.  `buf` alternates.
+    __device__ __forceinline__ void segment(int t0, int a, int b, SegmentLds<W> &sh, int buf, float &prob, int &cnt,
+                                            int &live) const {
+        const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        float acc[kSlots] = {0.f, 0.f, 0.f, 0.f};
+        int n = 0;
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) sh.red[wave][expert_of<VEC>(i)] = acc[i];
-    if (lane_id() == 0) sh.live[wave] = n;
-    for (int i = tid; i < (b - a) * k; i += 64 * W) {
-        const int t = a + i / k;
-        const int e = idx[(size_t)a * k + i];
-        if ((unsigned)e < (unsigned)E && token_live(q, t)) atomicAdd(&sh.hist[e], 1);
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + wave + u * W;
+            if (t >= a && t < b && on[u]) {
+                ++n;
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) acc[i] += p[u][i];
+            }
+        }
+        if (VEC) {
+            *(float4 *)&sh.red[buf][wave][4 * lane_id()] = float4{acc[0], acc[1], acc[2], acc[3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) sh.red[buf][wave][expert_of<VEC>(i)] = acc[i];
+        }
+        if (lane_id() == 0) sh.live[buf][wave] = n;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (e[i] >= 0 && te[i] >= a && te[i] < b) atomicAdd(&sh.hist[buf][e[i]], 1);
+        __syncthreads();
+        prob = 0.0f;
+        cnt = 0;
+        live = 0;
+        if (tid < kMaxExperts) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) live += sh.live[buf][w];
+#pragma unroll
+            for (int w = 0; w < W; ++w) prob += sh.red[buf][w][tid];
+            cnt = sh.hist[buf][tid];
+            sh.hist[buf][tid] = 0;  // for the segment after the next, past its barrier
+        }
     }
-    __syncthreads();
-    prob = 0.0f;
-    cnt = 0;
-    live = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) live += sh.live[w];
-    if (tid < kMaxExperts) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) prob += sh.red[w][tid];
-        cnt = sh.hist[tid];
-    }
-    __syncthreads();  // the next segment writes the arrays again
-}
+};
 
-// One workgroup per chunk of C tokens; a chunk's segments (one per sequence
-// that it meets) go to partial sum c + s, which no other segment shares.
-template <bool VEC>
-__global__ __launch_bounds__(256) void k_balance_part(Seqs q, const float *__restrict__ logits,
-                                                      const int32_t *__restrict__ idx, int E, int k, int C, Parts p) {
-    __shared__ SegmentLds<VEC, 4> sh;
-    const int t0 = blockIdx.x * C, t1 = min(t0 + C, q.T);
+// One workgroup per chunk of C = W U tokens; a chunk's segments go to partial
+// sum c + s, which no other segment shares.
+template <bool VEC, int W, int U>
+__global__ __launch_bounds__(64 * W) void k_balance_part(Seqs q, const float *__restrict__ logits,
+                                                         const int32_t *__restrict__ idx, int E, int k, Parts p) {
+    __shared__ __attribute__((aligned(16))) SegmentLds<W> sh;
+    const int t0 = blockIdx.x * (W * U), t1 = min(t0 + W * U, q.T);
+    const int tid = threadIdx.x;
+    if (tid < kMaxExperts) sh.hist[0][tid] = sh.hist[1][tid] = 0;
+    Tokens<VEC, W, U> tok;
+    tok.load(q, logits, idx, E, k, t0, t1);
+    __syncthreads();
+    int buf = 0;
     for (int s = seq_of(q, t0); s < q.n; ++s) {
-        const int a = max(seq_begin(q, s), t0), b = min(seq_end(q, s), t1);
-        if (seq_begin(q, s) >= t1) break;
+        const int begin = seq_begin(q, s), a = max(begin, t0), b = min(seq_end(q, s), t1);
+        if (begin >= t1) break;
         if (a >= b) continue;
         float prob;
         int cnt, live;
-        segment_sums<VEC, 4>(q, logits, idx, E, k, a, b, sh, prob, cnt, live);
+        tok.segment(t0, a, b, sh, buf, prob, cnt, live);
+        buf ^= 1;
         const size_t row = (size_t)blockIdx.x + s;
-        if ((int)threadIdx.x < E) {
-            p.prob[row * E + threadIdx.x] = prob;
-            p.cnt[row * E + threadIdx.x] = cnt;
+        if (tid < E) {
+            p.prob[row * E + tid] = prob;
+            p.cnt[row * E + tid] = cnt;
         }
-        if (threadIdx.x == 0) p.live[row] = live;
+        if (tid == 0) p.live[row] = live;
+        if (b == t1) break;  // the chunk ends in this sequence
     }
 }
 
@@ -290,71 +331,92 @@ __global__ __launch_bounds__(64 * GR) void k_balance_reduce(Seqs q, int E, int k
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d, kWave);
         if (tid == 0) {
-            __hip_atomic_store(&p.dot[(size_t)s * EB + eb], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (eb == 0) __hip_atomic_store(&p.nq[s], live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            last = __hip_atomic_fetch_add(p.counter, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+            // The sums go to memory by atomic exchanges whose results are
+            // waited for, then the arrival is counted: whoever sees the last
+            // count and reads with atomic loads reads the sums, with no
+            // write-back of the whole L2 (a releasing count took 3 us more).
+            const double was = __hip_atomic_exchange(&p.dot[(size_t)s * EB + eb], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (eb == 0) {
+                const int nwas = __hip_atomic_exchange(&p.nq[s], live, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                asm volatile("" ::"v"(nwas) : "memory");
+            }
+            asm volatile("" ::"v"(was) : "memory");
+            last = __hip_atomic_fetch_add(p.counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                    (int)gridDim.x - 1;
         }
     }
     __syncthreads();
     if (!last) return;
-    __threadfence();
+    if (tid == 0) __hip_atomic_store(p.counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    auto dot_of = [&](int i) {
+        double d = 0.0;
+        for (int j = 0; j < EB; ++j)
+            d += __hip_atomic_load(&p.dot[(size_t)i * EB + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return d;
+    };
     auto nq_of = [&](int i) { return __hip_atomic_load(&p.nq[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+    if (q.n <= kWave) {  // a lane per sequence
+        if (tid >= kWave) return;
+        const int n = tid < q.n ? nq_of(tid) : 0;
+        const double c = coef_of(alpha, E, k, n, __popcll(__ballot(n > 0)));
+        if (tid < q.n) o.coef[tid] = (float)c;
+        double sum = c != 0.0 ? c * dot_of(tid) : 0.0;
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+        if (tid == 0) *o.loss = (float)sum;
+        return;
+    }
     int some = 0;
     for (int i = tid; i < q.n; i += NT) some += nq_of(i) > 0;
     const int total = (int)block_sum<NT>((double)some, sd);
     double sum = 0.0;
     for (int i = tid; i < q.n; i += NT) {
         const double c = coef_of(alpha, E, k, nq_of(i), total);
-        double d = 0.0;
-        for (int j = 0; j < EB; ++j)
-            d += __hip_atomic_load(&p.dot[(size_t)i * EB + j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         o.coef[i] = (float)c;
-        sum += c != 0.0 ? c * d : 0.0;
+        sum += c != 0.0 ? c * dot_of(i) : 0.0;
     }
     sum = block_sum<NT>(sum, sd);
-    if (tid == 0) {
-        *o.loss = (float)sum;
-        __hip_atomic_store(p.counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+    if (tid == 0) *o.loss = (float)sum;
 }
 
-// Few tokens and sequences: everything in one workgroup.
-template <bool VEC>
-__global__ __launch_bounds__(512) void k_balance_one(Seqs q, const float *__restrict__ logits,
-                                                     const int32_t *__restrict__ idx, int E, int k, float alpha, Out o) {
-    __shared__ SegmentLds<VEC, 8> sh;
-    __shared__ double sdot[kOneSeqs], sd[8];
+// Few tokens and sequences: everything in one workgroup, in one launch.
+template <bool VEC, int U>
+__global__ __launch_bounds__(1024) void k_balance_one(Seqs q, const float *__restrict__ logits,
+                                                      const int32_t *__restrict__ idx, int E, int k, float alpha,
+                                                      Out o) {
+    constexpr int W = 16;
+    __shared__ __attribute__((aligned(16))) SegmentLds<W> sh;
+    __shared__ double sdot[kOneSeqs][4];
     __shared__ int snq[kOneSeqs];
     const int tid = threadIdx.x;
+    if (tid < kMaxExperts) sh.hist[0][tid] = sh.hist[1][tid] = 0;
+    Tokens<VEC, W, U> tok;
+    tok.load(q, logits, idx, E, k, 0, q.T);
+    __syncthreads();
     for (int s = 0; s < q.n; ++s) {
-        const int a = seq_begin(q, s), b = seq_end(q, s);
-        float prob = 0.0f;
-        int cnt = 0, live = 0;
-        if (a < b) segment_sums<VEC, 8>(q, logits, idx, E, k, a, b, sh, prob, cnt, live);
-        double dot = 0.0;
-        if (tid < E) {
-            o.counts[(size_t)s * E + tid] = cnt;
-            o.prob[(size_t)s * E + tid] = prob;
-            dot = (double)cnt * (double)prob;
-        }
+        float prob;
+        int cnt, live;
+        tok.segment(0, seq_begin(q, s), seq_end(q, s), sh, s & 1, prob, cnt, live);
+        if (tid < kMaxExperts) {
+            double dot = 0.0;
+            if (tid < E) {
+                o.counts[(size_t)s * E + tid] = cnt;
+                o.prob[(size_t)s * E + tid] = prob;
+                dot = (double)cnt * (double)prob;
+            }
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d, kWave);
-        if (lane_id() == 0) sd[tid >> 6] = dot;
-        __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < 8; ++w) dot += sd[w];
-            sdot[s] = dot;
-            snq[s] = live;
+            for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d, kWave);
+            if (lane_id() == 0) sdot[s][tid >> 6] = dot;
+            if (tid == 0) snq[s] = live;
         }
-        __syncthreads();
     }
+    __syncthreads();
     if (tid < kWave) {
         const int n = tid < q.n ? snq[tid] : 0;
         const int some = __popcll(__ballot(n > 0));
         const double c = coef_of(alpha, E, k, n, some);
         if (tid < q.n) o.coef[tid] = (float)c;
-        double sum = n > 0 && c != 0.0 ? c * sdot[tid] : 0.0;
+        double sum = n > 0 && c != 0.0 ? c * (((sdot[tid][0] + sdot[tid][1]) + sdot[tid][2]) + sdot[tid][3]) : 0.0;
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, kWave);
         if (tid == 0) *o.loss = (float)sum;
@@ -362,11 +424,25 @@ __global__ __launch_bounds__(512) void k_balance_one(Seqs q, const float *__rest
 }
 
 // ---------------------------------------------------------------- gradient
-// A wave takes TW consecutive tokens, four in flight.  Per token: the scores
-// of its experts, their sum S and the sum of c s (two wave reductions), the
-// balance term, and the k chosen experts' weight terms, computed by lanes
-// j < k from the chosen logits and handed to the lanes that hold them.
-template <bool VEC>
+// The sum over the eight lanes of each aligned group of eight, in every lane.
+__device__ __forceinline__ float sum8(float v) {
+#define MOE_DPP_ADD(CTRL) \
+    v = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false))
+    MOE_DPP_ADD(0xB1);   // quad_perm 1,0,3,2
+    MOE_DPP_ADD(0x4E);   // quad_perm 2,3,0,1
+    MOE_DPP_ADD(0x141);  // row_half_mirror
+#undef MOE_DPP_ADD
+    return v;
+}
+
+// A wave takes TW consecutive tokens, U of them at a time (1, or 8: the
+// requests of eight rows in flight).  The routing-weight term first, of all U
+// tokens at once: lane 8 u + j has token u's j-th choice, its score comes from
+// its logit by itself, the two sums over a token's choices are sums over
+// eight lanes, and the terms go to the lanes that hold those experts through
+// a row of zeros in LDS per token.  Then per token the scores of all experts,
+// their sum and the sum of c s (two wave reductions), and the balance term.
+template <bool VEC, int U>
 __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__restrict__ logits,
                                                         const int32_t *__restrict__ idx,
                                                         const int32_t *__restrict__ counts,
@@ -374,13 +450,15 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
                                                         const float *__restrict__ d_loss,
                                                         const float *__restrict__ d_w, int E, int k, float scale,
                                                         int TW, float *__restrict__ d_logits) {
-    constexpr int U = 4;
+    __shared__ __attribute__((aligned(16))) float sterm[4][U][kMaxExperts];
     const int l = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t0 = (blockIdx.x * 4 + wave) * TW, t1 = min(t0 + TW, q.T);
     if (t0 >= t1) return;
-    const float dl = d_loss ? *d_loss : 0.0f;
-    int s = seq_of(q, t0), begin = 0, end = 0;
+    float(&term)[U][kMaxExperts] = sterm[wave];
+    const int lu = l >> 3, lj = l & 7;  // the lane's token and choice
     float c[kSlots] = {0.f, 0.f, 0.f, 0.f};
+    int s = -1, begin = 0, end = 0;
+    float dl = 0.0f;
     auto enter = [&]() {  // the sequence s: its bounds and c of the lane's experts
         begin = s < q.n ? seq_begin(q, s) : q.T;
         end = s < q.n ? seq_end(q, s) : q.T;
@@ -391,28 +469,41 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
             c[i] = d_loss && s < q.n && e < E ? f * (float)counts[(size_t)s * E + e] : 0.0f;
         }
     };
-    enter();
+    if (d_w) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) *(float4 *)&term[u][4 * l] = float4{0.f, 0.f, 0.f, 0.f};
+    }
     for (int tb = t0; tb < t1; tb += U) {
-        float x[U][kSlots], xk[U], dw[U];
-        int ek[U];
+        float x[U][kSlots];
         bool on[U];
+        int ek = -1;
+        float dw = 0.0f, xk = 0.0f;
+        if (d_w && lu < U && lj < k && tb + lu < t1) {
+            ek = idx[(size_t)(tb + lu) * k + lj];
+            dw = d_w[(size_t)(tb + lu) * k + lj];
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int t = min(tb + u, t1 - 1);
             on[u] = token_live(q, t);
             load_row<VEC>(logits + (size_t)t * E, E, x[u]);
-            ek[u] = -1;
-            dw[u] = 0.0f;
-            if (d_w && l < k) {
-                ek[u] = idx[(size_t)t * k + l];
-                dw[u] = d_w[(size_t)t * k + l];
-            }
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = min(tb + u, t1 - 1);
-            if ((unsigned)ek[u] >= (unsigned)E) ek[u] = -1;
-            xk[u] = ek[u] >= 0 ? logits[(size_t)t * E + ek[u]] : 0.0f;
+        if (s < 0) {
+            dl = d_loss ? *d_loss : 0.0f;
+            s = seq_of(q, t0);
+            enter();
+        }
+        if ((unsigned)ek >= (unsigned)E) ek = -1;
+        if (d_w) {
+            if (ek >= 0) xk = logits[(size_t)(tb + lu) * E + ek];
+            const float sk = ek >= 0 ? score(xk) : 0.0f;
+            const float S = sum8(sk), A = sum8(ek >= 0 ? dw * sk : 0.0f);
+            const float ik = S == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(S);
+            // (the same index twice in a row: its terms add)
+            if (ek >= 0) atomicAdd(&term[lu < U ? lu : 0][ek], scale * ik * (dw - A * ik));
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -423,7 +514,19 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
                 enter();
             }
             const bool live = on[u] && s < q.n && t >= begin;
-            float slope[kSlots], sum = 0.0f, cs = 0.0f;
+            float slope[kSlots], sum = 0.0f, cs = 0.0f, ds[kSlots] = {0.f, 0.f, 0.f, 0.f};
+            if (d_w) {
+                if (VEC) {
+                    const float4 v = *(const float4 *)&term[u][4 * l];
+                    ds[0] = v.x;
+                    ds[1] = v.y;
+                    ds[2] = v.z;
+                    ds[3] = v.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kSlots; ++i) ds[i] = term[u][expert_of<VEC>(i)];
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
                 float sc = score(x[u][i], slope[i]);
@@ -431,25 +534,13 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
                 sum += sc;
                 cs = __builtin_fmaf(c[i], sc, cs);
             }
-            sum = route::wave_tree_sum(sum);
-            cs = route::wave_tree_sum(cs);
-            const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
-            const float mean = cs * inv;
-            float ds[kSlots];
+            if (d_loss) {
+                sum = route::wave_tree_sum(sum);
+                cs = route::wave_tree_sum(cs);
+                const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
+                const float mean = cs * inv;
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i) ds[i] = d_loss ? (c[i] - mean) * inv : 0.0f;
-            if (d_w) {
-                const float sk = ek[u] >= 0 ? score(xk[u]) : 0.0f;
-                const float S = route::wave_tree_sum(sk), A = route::wave_tree_sum(dw[u] * sk);
-                const float ik = S == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(S);
-                const float g = scale * ik * (dw[u] - A * ik);
-                for (int j = 0; j < k; ++j) {
-                    const int e = __builtin_amdgcn_readlane(ek[u], j);
-                    const float gj = route::readlane_f32(g, j);
-#pragma unroll
-                    for (int i = 0; i < kSlots; ++i)
-                        if (expert_of<VEC>(i) == e) ds[i] += gj;
-                }
+                for (int i = 0; i < kSlots; ++i) ds[i] = __builtin_fmaf(c[i] - mean, inv, ds[i]);
             }
             float *row = d_logits + (size_t)t * E;
 #pragma unroll
@@ -461,6 +552,15 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
                 for (int i = 0; i < kSlots; ++i)
                     if (expert_of<VEC>(i) < E) row[expert_of<VEC>(i)] = ds[i];
             }
+        }
+        if (d_w) {  // the rows are zeros again before the next tokens' terms
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            if (ek >= 0) term[lu < U ? lu : 0][ek] = 0.0f;
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
     }
 }
@@ -501,23 +601,27 @@ extern "C" moe_status moe_balance_loss(const moe_layer_desc *desc, int32_t T, in
     const Out o{counts, prob_sums, seq_coef, loss};
     const bool vec = E % 4 == 0 && aligned(logits, 16);
     if (T <= kOneTokens && n_seq <= kOneSeqs) {
-        if (vec)
-            hipLaunchKernelGGL(k_balance_one<true>, dim3(1), dim3(512), 0, st, q, logits, topk_idx, E, k, alpha, o);
-        else
-            hipLaunchKernelGGL(k_balance_one<false>, dim3(1), dim3(512), 0, st, q, logits, topk_idx, E, k, alpha, o);
+        const auto one = vec ? (T <= 32 ? k_balance_one<true, 2> : k_balance_one<true, 8>)
+                             : (T <= 32 ? k_balance_one<false, 2> : k_balance_one<false, 8>);
+        hipLaunchKernelGGL(one, dim3(1), dim3(1024), 0, st, q, logits, topk_idx, E, k, alpha, o);
         return launch_status();
     }
     const int C = chunk_tokens(T), chunks = chunk_count(T), EB = (E + 63) / 64;
     const Parts p = parts_of(ws, chunks, n_seq, E);
     if (chunks > 0) {
-        if (vec)
-            hipLaunchKernelGGL(k_balance_part<true>, dim3(chunks), dim3(256), 0, st, q, logits, topk_idx, E, k, C, p);
-        else
-            hipLaunchKernelGGL(k_balance_part<false>, dim3(chunks), dim3(256), 0, st, q, logits, topk_idx, E, k, C, p);
+        void (*part)(Seqs, const float *, const int32_t *, int, int, Parts) = nullptr;
+        switch (C) {
+            case 8: part = vec ? k_balance_part<true, 8, 1> : k_balance_part<false, 8, 1>; break;
+            case 16: part = vec ? k_balance_part<true, 16, 1> : k_balance_part<false, 16, 1>; break;
+            case 32: part = vec ? k_balance_part<true, 16, 2> : k_balance_part<false, 16, 2>; break;
+            case 64: part = vec ? k_balance_part<true, 16, 4> : k_balance_part<false, 16, 4>; break;
+            default: part = vec ? k_balance_part<true, 16, 8> : k_balance_part<false, 16, 8>; break;
+        }
+        hipLaunchKernelGGL(part, dim3(chunks), dim3(C == 8 ? 512 : 1024), 0, st, q, logits, topk_idx, E, k, p);
         MOE_TRY(launch_status());
     }
     // 16 groups of threads where a sequence spans many chunks, else 4
-    if (chunks > 16 * (int64_t)n_seq)
+    if (chunks > 8 * (int64_t)n_seq)
         hipLaunchKernelGGL(k_balance_reduce<16>, dim3(n_seq * EB), dim3(1024), 0, st, q, E, k, C, EB, alpha, p, o);
     else
         hipLaunchKernelGGL(k_balance_reduce<4>, dim3(n_seq * EB), dim3(256), 0, st, q, E, k, C, EB, alpha, p, o);
@@ -538,15 +642,15 @@ extern "C" moe_status moe_route_backward(const moe_layer_desc *desc, int32_t T, 
     const int E = desc->n_routed, k = desc->top_k;
     const Seqs q{seq_offsets, token_mask, n_seq, T};
     const bool vec = E % 4 == 0 && aligned(logits, 16) && aligned(d_logits, 16);
-    // four tokens per wave while that does not fill the card, else 16
-    const int TW = T <= 32768 ? 4 : 16;
+    // a token per wave while that takes at most eight waves per SIMD, else
+    // eight at a time (256 experts, 8192 tokens: 7.5 us either way and 3.4
+    // against 6.0 at 128; 16384: 13.2 against 11.8; 65536: 47 against 33)
+    const int TW = T <= 8192 ? 1 : T <= 32768 ? 8 : 16;
     const dim3 grid((unsigned)((T + 4 * TW - 1) / (4 * TW)));
     hipStream_t st = (hipStream_t)stream;
-    if (vec)
-        hipLaunchKernelGGL(k_route_backward<true>, grid, dim3(256), 0, st, q, logits, topk_idx, counts, seq_coef, d_loss,
-                           d_topk_w, E, k, desc->routed_scale, TW, d_logits);
-    else
-        hipLaunchKernelGGL(k_route_backward<false>, grid, dim3(256), 0, st, q, logits, topk_idx, counts, seq_coef,
-                           d_loss, d_topk_w, E, k, desc->routed_scale, TW, d_logits);
+    const auto back = vec ? (TW == 1 ? k_route_backward<true, 1> : k_route_backward<true, 8>)
+                          : (TW == 1 ? k_route_backward<false, 1> : k_route_backward<false, 8>);
+    hipLaunchKernelGGL(back, grid, dim3(256), 0, st, q, logits, topk_idx, counts, seq_coef, d_loss, d_topk_w, E, k,
+                       desc->routed_scale, TW, d_logits);
     return launch_status();
 }
