@@ -145,10 +145,13 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+_Tensor = torch.Tensor
+
+
 def _ptr(t, name, dtype, numel, optional=False):
     # the common case first: a call checks up to 17 tensors, and a decode
     # step's calls are bound by the host
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() >= numel:
+    if isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.numel() >= numel:
         return t.data_ptr()
     if t is None:
         if optional:

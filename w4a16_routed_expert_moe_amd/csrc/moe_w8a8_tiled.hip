@@ -3,15 +3,21 @@
 // the weight rows.
 //
 // Per 128-wide k step the tile's activation codes (128 bytes a row) go from
-// global memory straight into one of four LDS stages, two and a half steps
-// ahead, and every wave reads all of them; the weights, which no two waves of
-// a workgroup share, go from global memory into registers, four half steps
-// (64 k) ahead, so that per matrix instruction of 16 cycles only 1024 / NSW
-// bytes come out of LDS.  The sums are exact in int32, so the k
-// loop holds nothing but loads and matrix instructions; both scales are
-// applied in the epilogue.
+// global memory straight into one of ST LDS stages, ST - 1 steps ahead, and
+// every wave reads all of them; the weights, which no two waves of a
+// workgroup share, go from global memory into registers, PF half steps (64 k)
+// ahead, so that per matrix instruction of 16 cycles only 1024 / NSW bytes
+// come out of LDS.  The sums are exact in int32, so the k loop holds nothing
+// but loads and matrix instructions; both scales are applied in the epilogue.
 // The wave multiplies only the m-tiles (16 rows) that have rows: the count is
 // a constant of each instance of the k loop, chosen once per work item.
+//
+// What bounds it.  Many rows: power.  The matrix instruction alone, on random
+// bytes, runs at 3800 TOPS here (4950 on zeros); a dense 8192 x 4096 x 4096
+// product takes 115 to 120 us (2300 to 2400 TOPS), and the same k loop
+// without its loads 93.  Few rows per group: the weights' bytes (the layer's
+// experts at 512 tokens: 5.8 TB/s).
+#include <algorithm>
 #include <type_traits>
 
 #include "moe_w8a8.h"
@@ -20,22 +26,21 @@ namespace moe {
 namespace w8 {
 namespace {
 
-constexpr int kStages = 4;
-
 // Chunk c (16 bytes) of row r of a stage sits at chunk c ^ swz(r): the eight
 // rows of each parity that one 16-lane group of an operand read takes then
 // lie on eight distinct chunks (two 128-byte rows share the 64 banks).
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
 // The matrix instruction written as assembly, so that each accumulator stays
-// in its registers: with all 256 accumulation registers in use the compiler's
-// own form rotates the accumulators through copies.  The two wait states in
+// in its registers and the loads between the instructions stay where they are
+// written: the compiler's own form rotates the accumulators of a large tile
+// through copies.  The two wait states in
 // front cover a copy that the compiler may place before it (they pass in the
 // shadow of the previous instruction's 16 cycles); an accumulator comes up
 // again only after every other one, and mfma_drain precedes the first use of
 // the sums.
 __device__ __forceinline__ void mfma_acc(v4i &acc, u32x4 a, u32x4 b) {
-    asm volatile("s_nop 1\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    asm volatile("s_nop 1\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+v"(acc) : "v"(a), "v"(b));
 }
 __device__ __forceinline__ void mfma_drain() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
@@ -54,16 +59,16 @@ __device__ __forceinline__ bool dense_item(int NB, int TM, int R, TileItem &it) 
     return true;
 }
 
-template <int ACT, int NSW, int MC, int PF, int OCC>
+template <int ACT, int NSW, int MC, int PF, int ST, int OCC>
 __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
     constexpr int TM = 16 * MC;  // times 64 NSW weight rows
     constexpr int HSW = NSW / 2;
-    __shared__ u32x4 sA[kStages * TM * 8];
+    static_assert(2 * (ST - 2) * NSW < 64, "the wait counts 64 loads");
+    __shared__ u32x4 sA[ST * TM * 8];
     constexpr int NO = ACT == MOE_ACT_SWIGLU ? HSW : NSW;  // output subtiles per wave
     constexpr int NWS = NSW / 4 > 0 ? NSW / 4 : 1;         // weight scales per thread
     __shared__ int srow[TM];
     __shared__ float sas[TM], sws[256 * NWS];
-    if constexpr (NSW * MC >= 64) asm volatile("" ::: "a0");
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = lane_id();
     const int m = l & 15, q = l >> 4;
     TileItem it;
@@ -136,9 +141,8 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
 #pragma unroll
             for (int c = 0; c < C; ++c) av[c] = sA[stage * (TM * 8) + 128 * c + a_lane[h]];
         };
-        dma_a(0, 0);
-        dma_a(1, min(1, KG - 1));
-        dma_a(2, min(2, KG - 1));
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) dma_a(i, min(i, KG - 1));
 #pragma unroll
         for (int h = 0; h < PF; ++h) {
             const uint32_t o = boff(h);
@@ -146,7 +150,7 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
             for (int j = 0; j < NSW; ++j) b[h][j] = *(const u32x4 *)(wb[j] + o);
         }
         __builtin_amdgcn_sched_barrier(0);
-        // the activation loads of steps 0 to 2 have landed, then every wave's
+        // the activation loads of the first ST - 1 steps have landed, then every wave's
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(PF * NSW));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -165,31 +169,36 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
             }
         };
         int s0 = 0;  // the stage of step kg
+        // This wave's activation loads of step kg + 1 have landed: they are
+        // older than the weight loads of the last 2 (ST - 2) half steps.
+        // After the barrier every wave's have, and every wave is done with
+        // the stage of step kg - 1, which step kg + ST - 1 takes.
+        auto turn = [&](int kg) {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * (ST - 2) * NSW));
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            dma_a((s0 + ST - 1) & (ST - 1), min(kg + ST - 1, KG - 1));
+            __builtin_amdgcn_sched_barrier(0);
+            s0 = (s0 + 1) & (ST - 1);
+        };
         auto step = [&](u32x4(&bl)[NSW], u32x4(&bh)[NSW], int kg) {
             read_a(a1, s0, 1);
             half(bl, a0, 2 * kg + PF);
-            __builtin_amdgcn_sched_barrier(0);
-            // This wave's activation loads of step kg + 1 have landed: they
-            // are older than the weight loads of the last four half steps.
-            // After the barrier every wave's have, and every wave is done
-            // with the stage of step kg - 1, which step kg + 3 takes.
-            __builtin_amdgcn_s_waitcnt(vmcnt_imm(4 * NSW));
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-            dma_a((s0 + 3) & 3, min(kg + 3, KG - 1));
-            __builtin_amdgcn_sched_barrier(0);
-            s0 = (s0 + 1) & 3;
+            turn(kg);
             read_a(a0, s0, 0);
             half(bh, a1, 2 * kg + PF + 1);
             __builtin_amdgcn_sched_barrier(0);
         };
+        constexpr int NS = PF / 2;  // steps whose weights are in registers
         int kg = 0;
 #pragma unroll 1
-        for (; kg + 1 < KG; kg += 2) {
-            step(b[0], b[1], kg);
-            step(b[PF - 2], b[PF - 1], kg + 1);
-        }
-        if (kg < KG) step(b[0], b[1], kg);
+        for (; kg + NS <= KG; kg += NS)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) step(b[2 * i], b[2 * i + 1], kg + i);
+#pragma unroll
+        for (int i = 0; i < NS - 1; ++i)
+            if (kg + i < KG) step(b[2 * i], b[2 * i + 1], kg + i);
         mfma_drain();
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load into LDS outlives the block
 
@@ -258,49 +267,62 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
     }
 }
 
-template <int NSW, int MC, int PF, int OCC>
+template <int NSW, int MC, int PF, int ST, int OCC>
 void launch(int act, Args a, hipStream_t st) {
     constexpr int TM = 16 * MC;
     a.NB = (a.NT + 4 * NSW - 1) / (4 * NSW);
     int64_t tiles = a.offsets ? (int64_t)a.R / TM + (a.R < a.G ? a.R : a.G) : (a.R + TM - 1) / TM;
     if (tiles > a.R) tiles = a.R;  // every tile has a row
     const dim3 grid((unsigned)((tiles * a.NB + 7) / 8 * 8));  // a whole slice per XCD
-    if (act == MOE_ACT_SWIGLU)
-        hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_SWIGLU, NSW, MC, PF, OCC>), grid, dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_NONE, NSW, MC, PF, OCC>), grid, dim3(256), 0, st, a);
+    if constexpr (NSW > 1) {  // SwiGLU: a gate and an up subtile per wave at least
+        if (act == MOE_ACT_SWIGLU) {
+            hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_SWIGLU, NSW, MC, PF, ST, OCC>), grid, dim3(256), 0, st, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_NONE, NSW, MC, PF, ST, OCC>), grid, dim3(256), 0, st, a);
 }
 
 }  // namespace
 
-// Which tile: the largest that leaves few CUs without a workgroup, for a
-// larger tile reads fewer bytes per product.  Dense, us (N = K = 4096; tiles
-// of rows x weight rows):
-//   rows       128 x 256   64 x 256   64 x 128   32 x 128
-//   61              18.1       16.7       12.2        9.8
-//   256             28.5       17.0       12.8       10.6
-//   512             29.0       17.9       13.9       17.7
-//   1024            30.0       21.7       22.6       31.6
+// Which tile: the one with the least cost times rounds of one workgroup per
+// CU.  A larger tile reads fewer bytes per product (what bounds a CU that has
+// its workgroup), a smaller one fills the CUs with fewer rows; a second
+// workgroup on some of the CUs costs nearly a second round.  The costs are
+// the times of one round at N = K = 4096, 8 to 30 us; measured there, us
+// (tiles of rows x weight rows):
+//   rows       128 x 256   64 x 256   64 x 128   32 x 128   32 x 64
+//   61              18.1       16.7       12.2        9.8       7.7
+//   256             28.5       17.0       12.8       10.6      12.6
+//   512             29.0       17.9       13.9       17.7      22.6
+//   1024            30.0       21.7       22.6       31.6      40.7
 //   2048            36.9       40.5       46.9       61.6
-//   8192             119        149        169        246
+//   8192             119        149        169        246       293
+// (32 x 64 without an activation only: a wave has one subtile.)
 // Groups of few rows are bound by the weights' bytes: 64 x 128 tiles keep the
 // most of them in flight (the layer's experts at hidden 4096, 256 experts, 6
 // per token: 1162 us against 1177 with 128 x 256 at 1024 tokens, 1279 against
 // 1249 at 2048, where a group has 48 rows).
 void launch_tiled(int act, Args a, hipStream_t st) {
-    auto fills = [&](int TM, int TN) {
+    auto cost = [&](int TM, int TN, int of_a_round) {
         const int64_t tiles = (a.R + TM - 1) / TM + (a.offsets ? (a.R < a.G ? a.R : a.G) / 2 : 0);
-        return tiles * ((16 * a.NT + TN - 1) / TN) >= 160;
+        return (tiles * ((16 * a.NT + TN - 1) / TN) + 255) / 256 * of_a_round;
     };
-    const bool few = a.offsets && a.R < 48 * (int64_t)a.G;
-    if (!few && fills(128, 256))
-        launch<4, 8, 2, 2>(act, a, st);
-    else if (!few && fills(64, 256))
-        launch<4, 4, 4, 2>(act, a, st);
-    else if (fills(64, 128))
-        launch<2, 4, 4, 3>(act, a, st);
+    const int64_t c128x256 = cost(128, 256, 30), c64x256 = cost(64, 256, 20), c64x128 = cost(64, 128, 12),
+                  c32x128 = cost(32, 128, 10), c32x64 = act == MOE_ACT_NONE ? cost(32, 64, 8) : INT64_MAX;
+    const int64_t least = std::min({c128x256, c64x256, c64x128, c32x128, c32x64});
+    if (a.offsets && a.R < 48 * (int64_t)a.G)
+        launch<2, 4, 4, 4, 3>(act, a, st);
+    else if (c128x256 == least)
+        launch<4, 8, 2, 4, 2>(act, a, st);
+    else if (c64x256 == least)
+        launch<4, 4, 4, 4, 2>(act, a, st);
+    else if (c64x128 == least)
+        launch<2, 4, 4, 4, 3>(act, a, st);
+    else if (c32x128 == least)
+        launch<2, 2, 4, 4, 4>(act, a, st);
     else
-        launch<2, 2, 4, 4>(act, a, st);
+        launch<1, 2, 8, 8, 4>(act, a, st);
 }
 
 }  // namespace w8
