@@ -302,18 +302,19 @@ void launch(int act, Args a, hipStream_t st) {
 // Groups of few rows are bound by the weights' bytes: 64 x 128 tiles keep the
 // most of them in flight (the layer's experts at hidden 4096, 256 experts, 6
 // per token: 1162 us against 1177 with 128 x 256 at 1024 tokens, 1279 against
-// 1249 at 2048, where a group has 48 rows).
+// 1249 at 2048, where a group has 48 rows; 64 x 256 there: 1282).
 void launch_tiled(int act, Args a, hipStream_t st) {
-    auto cost = [&](int TM, int TN, int of_a_round) {
+    auto workgroups = [&](int TM, int TN) {
         const int64_t tiles = (a.R + TM - 1) / TM + (a.offsets ? (a.R < a.G ? a.R : a.G) / 2 : 0);
-        return (tiles * ((16 * a.NT + TN - 1) / TN) + 255) / 256 * of_a_round;
+        return tiles * ((16 * a.NT + TN - 1) / TN);
     };
+    auto cost = [&](int TM, int TN, int of_a_round) { return (workgroups(TM, TN) + 255) / 256 * of_a_round; };
     const int64_t c128x256 = cost(128, 256, 30), c64x256 = cost(64, 256, 20), c64x128 = cost(64, 128, 12),
                   c32x128 = cost(32, 128, 10), c32x64 = act == MOE_ACT_NONE ? cost(32, 64, 8) : INT64_MAX;
     const int64_t least = std::min({c128x256, c64x256, c64x128, c32x128, c32x64});
     if (a.offsets && a.R < 48 * (int64_t)a.G)
         launch<2, 4, 4, 4, 3>(act, a, st);
-    else if (c128x256 == least)
+    else if (c128x256 == least || (a.offsets && workgroups(128, 256) >= 256))
         launch<4, 8, 2, 4, 2>(act, a, st);
     else if (c64x256 == least)
         launch<4, 4, 4, 4, 2>(act, a, st);
