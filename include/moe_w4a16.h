@@ -515,7 +515,8 @@ moe_status moe_w8a8_gemm(int32_t M, int32_t N, int32_t K, const int8_t *a, const
 /* where it is used.                                                         */
 /*   x          bf16 [M][K], 16-byte aligned                                 */
 /*   codes, scales  scratch: int8 [M][K] (16-byte aligned) and fp32 [M];     */
-/*              their contents afterwards are unspecified                    */
+/*              their contents afterwards are unspecified (calls that may    */
+/*              overlap in time need distinct ones)                          */
 /*   the rest as moe_w8a8_gemm                                               */
 moe_status moe_w8a8_linear(int32_t M, int32_t N, int32_t K, const uint16_t *x,
                            const int8_t *w_packed, const float *w_scales, int8_t *codes,

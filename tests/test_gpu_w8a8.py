@@ -165,6 +165,13 @@ def test_gemm_bit_exact(M, N, K):
     assert (out[M:] == 7.0).all()  # rows behind the last one: as they were
 
 
+# wide enough outputs that the rows choose each of the tiles: 32 x 64, 32 x 128, 64 x 128, 64 x 256, 128 x 256
+@pytest.mark.parametrize("M", [40, 200, 300, 640, 1100, 1500])
+@pytest.mark.parametrize("N,K", [(4096, 16), (4096, 400), (4112, 640)])
+def test_gemm_every_tile(M, N, K):
+    test_gemm_bit_exact(M, N, K)
+
+
 @pytest.mark.parametrize("M", [1, 40, 200])
 def test_gemm_extreme_codes(M):
     """The largest sums: 65536 products of -128 and -128 (2^30)."""
@@ -237,6 +244,8 @@ def _groups(rng, G, R, empty):
     (40, 12, 3, 1, 256, 256, True), (64, 5, 2, 1, 512, 144, False), (65, 6, 2, 1, 640, 400, True),
     (200, 3, 2, 1, 1152, 512, True), (421, 40, 3, 1, 1024, 1024, True), (500, 200, 6, 0, 128, 128, True),
     (700, 1, 1, 1, 1024, 2064, False),
+    (300, 1, 1, 1, 256, 272, True), (1200, 1, 1, 1, 1024, 400, True), (2500, 1, 1, 1, 2048, 144, True),
+    (2500, 3, 2, 1, 1024, 80, False), (900, 4, 2, 0, 4096, 48, True),
 ])
 @pytest.mark.parametrize("act", [moe.MOE_ACT_NONE, moe.MOE_ACT_SWIGLU])
 def test_grouped_every_element(T, E, k, ns, N, K, gather, act):
@@ -329,6 +338,42 @@ def test_layer_stage_by_stage(T, H, I, E, k, ns):
     want = terms.sum(1)
     bound = 2.0 ** -8 * np.abs(want) + (k + 2) * 2.0 ** -24 * np.abs(terms).sum(1) * 2
     assert (np.abs(_f32(bf16_to_np_bits(buf.out)) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("T", [1, 3, 600, 3000])
+def test_full_size_layer(T):
+    """The layer at hidden 4096, inter 2048, 256 experts, 6 per token: sampled rows of h, y and out from the codes."""
+    H, I, E, k = 4096, 2048, 256, 6
+    case = Case("shape", T=T, H=H, E=E, k=k, I=I, n_shared=1, seed=3)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+    G = E + 1
+    w13 = torch.empty((G, 2 * I, H), dtype=torch.int8, device="cuda")
+    w2 = torch.empty((G, H, I), dtype=torch.int8, device="cuda")
+    for g in range(G):
+        w13[g] = torch.randint(-127, 128, (2 * I, H), device="cuda", generator=gen, dtype=torch.int8)
+        w2[g] = torch.randint(-127, 128, (H, I), device="cuda", generator=gen, dtype=torch.int8)
+    s13 = (torch.rand((G, 2 * I), device="cuda", generator=gen) + 0.5) / (74 * 64)
+    s2 = (torch.rand((G, H), device="cuda", generator=gen) + 0.5) / (74 * 45)
+    experts = moe.ExpertWeights(w13=moe.prepack(w13, G, 2 * I, H, fmt="int8"), s13=s13,
+                                w2=moe.prepack(w2, G, H, I, fmt="int8"), s2=s2, fmt="int8")
+    layer = moe.MoELayer(case.desc, case.layer_obj.w_router, case.layer_obj.gate_bias, experts)
+    buf = moe.Buffers(case.desc, T, int8=True)
+    layer.forward(case.xd, buf)
+    torch.cuda.synchronize()
+    off, tok = buf.group_offsets.cpu().numpy(), buf.sorted_token.cpu().numpy()
+    R = case.desc.rows(T)
+    rows = np.unique(np.concatenate([np.arange(min(R, 6)), [R - 1, R - T], np.random.default_rng(T).integers(0, R, 40)]))
+    h, y = bf16_to_np_bits(buf.h[rows]), bf16_to_np_bits(buf.y[rows])
+    xc, xs = _quant_ref(case.x[tok[rows]])
+    hc, hs = _quant_ref(h)
+    for i, r in enumerate(rows):
+        g = int(np.searchsorted(off, r, side="right") - 1)
+        v = _int_product(xc[i:i + 1], w13[g].cpu().numpy())[0] * float(xs[i]) * s13[g].double().cpu().numpy()
+        want = v[:I] / (1 + np.exp(-v[:I])) * v[I:]
+        assert (np.abs(_f32(h[i]) - want) <= SWIGLU_TOL * np.abs(want) + 1e-30).all()
+        acc = _int_product(hc[i:i + 1], w2[g].cpu().numpy())
+        assert np.array_equal(_f32(y[i:i + 1]), _f32(_scaled(acc, hs[i:i + 1], s2[g].cpu().numpy())))
 
 
 @pytest.mark.parametrize("T", [1, 8, 40, 200])
