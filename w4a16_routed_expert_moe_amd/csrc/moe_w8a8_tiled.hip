@@ -7,7 +7,8 @@
 // every wave reads all of them; the weights, which no two waves of a
 // workgroup share, go from global memory into registers, PF half steps (64 k)
 // ahead, so that per matrix instruction of 16 cycles only 1024 / NSW bytes
-// come out of LDS.  The sums are exact in int32, so the k loop holds nothing
+// come out of LDS.  ONCE: groups of one tile, whose weights are read by one
+// workgroup and not kept in the caches.  The sums are exact in int32, so the k loop holds nothing
 // but loads and matrix instructions; both scales are applied in the epilogue.
 // The wave multiplies only the m-tiles (16 rows) that have rows: the count is
 // a constant of each instance of the k loop, chosen once per work item.
@@ -59,7 +60,7 @@ __device__ __forceinline__ bool dense_item(int NB, int TM, int R, TileItem &it) 
     return true;
 }
 
-template <int ACT, int NSW, int MC, int PF, int ST, int OCC>
+template <int ACT, int NSW, int MC, int PF, int ST, int OCC, bool ONCE>
 __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
     constexpr int TM = 16 * MC;  // times 64 NSW weight rows
     constexpr int HSW = NSW / 2;
@@ -136,6 +137,9 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
 #pragma unroll
             for (int j = 0; j < NSW; ++j) acc[c][j] = v4i{0, 0, 0, 0};
         u32x4 b[PF][NSW], a0[C], a1[C];  // the weights of PF half steps
+        auto load_b = [](const int8_t *at) {
+            return ONCE ? __builtin_nontemporal_load((const u32x4 *)at) : *(const u32x4 *)at;
+        };
         auto boff = [&](int kb) { return (uint32_t)min(kb, KB - 1) * kBlockBytes + 16 * l; };
         auto read_a = [&](u32x4(&av)[C], int stage, int h) {
 #pragma unroll
@@ -147,7 +151,7 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
         for (int h = 0; h < PF; ++h) {
             const uint32_t o = boff(h);
 #pragma unroll
-            for (int j = 0; j < NSW; ++j) b[h][j] = *(const u32x4 *)(wb[j] + o);
+            for (int j = 0; j < NSW; ++j) b[h][j] = load_b(wb[j] + o);
         }
         __builtin_amdgcn_sched_barrier(0);
         // the activation loads of the first ST - 1 steps have landed, then every wave's
@@ -165,7 +169,7 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
             for (int j = 0; j < NSW; ++j) {
 #pragma unroll
                 for (int c = 0; c < C; ++c) mfma_acc(acc[c][j], bv[j], av[c]);
-                bv[j] = *(const u32x4 *)(wb[j] + o);
+                bv[j] = load_b(wb[j] + o);
             }
         };
         int s0 = 0;  // the stage of step kg
@@ -267,7 +271,7 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
     }
 }
 
-template <int NSW, int MC, int PF, int ST, int OCC>
+template <int NSW, int MC, int PF, int ST, int OCC, bool ONCE = false>
 void launch(int act, Args a, hipStream_t st) {
     constexpr int TM = 16 * MC;
     a.NB = (a.NT + 4 * NSW - 1) / (4 * NSW);
@@ -276,11 +280,11 @@ void launch(int act, Args a, hipStream_t st) {
     const dim3 grid((unsigned)((tiles * a.NB + 7) / 8 * 8));  // a whole slice per XCD
     if constexpr (NSW > 1) {  // SwiGLU: a gate and an up subtile per wave at least
         if (act == MOE_ACT_SWIGLU) {
-            hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_SWIGLU, NSW, MC, PF, ST, OCC>), grid, dim3(256), 0, st, a);
+            hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_SWIGLU, NSW, MC, PF, ST, OCC, ONCE>), grid, dim3(256), 0, st, a);
             return;
         }
     }
-    hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_NONE, NSW, MC, PF, ST, OCC>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((k_w8a8_tiled<MOE_ACT_NONE, NSW, MC, PF, ST, OCC, ONCE>), grid, dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -302,7 +306,13 @@ void launch(int act, Args a, hipStream_t st) {
 // Groups of few rows are bound by the weights' bytes: 64 x 128 tiles keep the
 // most of them in flight (the layer's experts at hidden 4096, 256 experts, 6
 // per token: 1162 us against 1177 with 128 x 256 at 1024 tokens, 1279 against
-// 1249 at 2048, where a group has 48 rows; 64 x 256 there: 1282).
+// 1249 at 2048, where a group has 48 rows; 64 x 256 there: 1282), and loads
+// that pass the caches by stream them faster (512 tokens: 1057 against 1110
+// us; 8 tokens: 196 against 207; with a skewed choice of experts 491 against
+// 519 at 64 tokens, 1101 against 1064 at 512).  Not where several tiles share
+// a group's weights (8192 tokens: 2824 against 1990), nor where the layer's
+// weights may still be in the 256 MB last-level cache from the call before
+// (hidden 1024, 40 experts, 43 MB: 34.8 against 30.5 us at 421 tokens).
 void launch_tiled(int act, Args a, hipStream_t st) {
     auto workgroups = [&](int TM, int TN) {
         const int64_t tiles = (a.R + TM - 1) / TM + (a.offsets ? (a.R < a.G ? a.R : a.G) / 2 : 0);
@@ -312,7 +322,10 @@ void launch_tiled(int act, Args a, hipStream_t st) {
     const int64_t c128x256 = cost(128, 256, 30), c64x256 = cost(64, 256, 20), c64x128 = cost(64, 128, 12),
                   c32x128 = cost(32, 128, 10), c32x64 = act == MOE_ACT_NONE ? cost(32, 64, 8) : INT64_MAX;
     const int64_t least = std::min({c128x256, c64x256, c64x128, c32x128, c32x64});
-    if (a.offsets && a.R < 48 * (int64_t)a.G)
+    const size_t weights = (size_t)a.G * a.NT * a.KB * kBlockBytes;
+    if (a.offsets && a.R < 48 * (int64_t)a.G && weights >= (size_t)128 << 20)
+        launch<2, 4, 4, 4, 3, true>(act, a, st);
+    else if (a.offsets && a.R < 48 * (int64_t)a.G)
         launch<2, 4, 4, 4, 3>(act, a, st);
     else if (c128x256 == least || (a.offsets && workgroups(128, 256) >= 256))
         launch<4, 8, 2, 4, 2>(act, a, st);
