@@ -236,6 +236,27 @@ def test_ids_outside_are_not_counted_and_repeats_add():
     assert torch.isfinite(st.d_logits).all()
 
 
+def test_nothing_is_left_where_it_cancels():
+    """One choice per token: its weight is constant, its gradient exactly zero.  Nearly even counts: the balance term is
+    a small difference, still within 1e-6 of its own 2-norm (its parts are about 40 times larger than it; a difference
+    formed after rounding them would be off by 40 2^-23)."""
+    rng = np.random.default_rng(12)
+    x, idx = _inputs(rng, 300, 40, 1)
+    d_w = rng.standard_normal((300, 1)).astype(np.float32)
+    st = Step(x, idx, np.array([0, 300]), None, 1, d_loss=None, d_w=d_w).run()
+    torch.cuda.synchronize()
+    assert (st.d_logits[:-1] == 0).all()
+    x = (rng.standard_normal((1280, 64)) * 0.02).astype(np.float32)
+    idx = np.stack([np.arange(1280) % 64, (np.arange(1280) + 7) % 64], 1)
+    idx[:40, 0] = (idx[:40, 0] + 1) % 64
+    idx[0] = [5, 9]
+    st = Step(x, idx, np.array([0, 1280]), None, 2).run()
+    torch.cuda.synchronize()
+    grad = _reference(x, idx, np.array([0, 1280]), None, 2, 0.01, 1.0, 1.0, None)[4]
+    got = st.d_logits[:-1].double().cpu().numpy()
+    assert np.linalg.norm(got - grad) <= 1e-6 * np.linalg.norm(grad)
+
+
 def test_same_bits_every_call():
     rng = np.random.default_rng(7)
     x, idx = _inputs(rng, 9000, 256, 6)

@@ -424,15 +424,32 @@ __global__ __launch_bounds__(1024) void k_balance_one(Seqs q, const float *__res
 }
 
 // ---------------------------------------------------------------- gradient
-// The sum over the eight lanes of each aligned group of eight, in every lane.
-__device__ __forceinline__ float sum8(float v) {
-#define MOE_DPP_ADD(CTRL) \
-    v = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false))
-    MOE_DPP_ADD(0xB1);   // quad_perm 1,0,3,2
-    MOE_DPP_ADD(0x4E);   // quad_perm 2,3,0,1
-    MOE_DPP_ADD(0x141);  // row_half_mirror
-#undef MOE_DPP_ADD
+// v of the lane whose number differs in the bits of X, within each aligned
+// group of eight lanes.
+template <int X>
+__device__ __forceinline__ float lane_xor(float v) {
+    if constexpr (X >= 4) {  // row_half_mirror is X = 7
+        return lane_xor<7 - X>(__uint_as_float(route::dpp32<0x141>(__float_as_uint(v))));
+    } else if constexpr (X > 0) {  // quad_perm 0^X, 1^X, 2^X, 3^X
+        return __uint_as_float(route::dpp32<(0 ^ X) | (1 ^ X) << 2 | (2 ^ X) << 4 | (3 ^ X) << 6>(__float_as_uint(v)));
+    }
     return v;
+}
+// The routing-weight term of a token, whose choices (score s, gradient g of
+// the weight) sit in eight lanes: (g_j - sum_l g_l s_l / S) / S, written
+// sum_l s_l (g_j - g_l) / S^2 so that nothing cancels (one choice gives 0).
+__device__ __forceinline__ float weight_term(float s, float g) {
+    float S = s, d = 0.0f;
+#define MOE_PAIR(X)                                \
+    {                                                             \
+        const float so = lane_xor<X>(s), go = lane_xor<X>(g);     \
+        S += so;                                                  \
+        d = so != 0.0f ? __builtin_fmaf(so, g - go, d) : d;       \
+    }
+    MOE_PAIR(1) MOE_PAIR(2) MOE_PAIR(3) MOE_PAIR(4) MOE_PAIR(5) MOE_PAIR(6) MOE_PAIR(7)
+#undef MOE_PAIR
+    const float r = S == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(S);
+    return d * r * r;
 }
 
 // A wave takes TW consecutive tokens, U of them at a time (1, or 8: the
@@ -459,15 +476,23 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
     float c[kSlots] = {0.f, 0.f, 0.f, 0.f};
     int s = -1, begin = 0, end = 0;
     float dl = 0.0f;
-    auto enter = [&]() {  // the sequence s: its bounds and c of the lane's experts
+    // The sequence s: its bounds and c of the lane's experts, less their
+    // average: c[e] - sum_j c[j] p[j] is the same for c less any constant, and
+    // with nearly even counts little is left to cancel.
+    auto enter = [&]() {
         begin = s < q.n ? seq_begin(q, s) : q.T;
         end = s < q.n ? seq_end(q, s) : q.T;
-        const float f = d_loss && s < q.n ? dl * coef[s] : 0.0f;
+        if (!d_loss || s >= q.n) return;
+        float n[kSlots], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
             const int e = expert_of<VEC>(i);
-            c[i] = d_loss && s < q.n && e < E ? f * (float)counts[(size_t)s * E + e] : 0.0f;
+            n[i] = e < E ? (float)counts[(size_t)s * E + e] : 0.0f;
+            sum += n[i];
         }
+        const float f = dl * coef[s], even = __builtin_rintf(route::wave_tree_sum(sum) / (float)E);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) c[i] = expert_of<VEC>(i) < E ? f * (n[i] - even) : 0.0f;
     };
     if (d_w) {
 #pragma unroll
@@ -497,10 +522,9 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
         if (d_w) {
             if (ek >= 0) xk = logits[(size_t)(tb + lu) * E + ek];
             const float sk = ek >= 0 ? score(xk) : 0.0f;
-            const float S = sum8(sk), A = sum8(ek >= 0 ? dw * sk : 0.0f);
-            const float ik = S == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(S);
+            const float term_k = weight_term(sk, dw);
             // (the same index twice in a row: its terms add)
-            if (ek >= 0) atomicAdd(&term[lu < U ? lu : 0][ek], scale * ik * (dw - A * ik));
+            if (ek >= 0) atomicAdd(&term[lu < U ? lu : 0][ek], scale * term_k);
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
