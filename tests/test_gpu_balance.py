@@ -327,6 +327,39 @@ def test_graph_and_side_stream(T, S):
             assert torch.equal(getattr(st, name), getattr(eager, name)), name
 
 
+def test_many_tokens():
+    """More chunks of tokens than the partial sums' table has at its usual size, and a gradient past 16 tokens per wave:
+    sums against fp64, the gradient at sampled tokens."""
+    T, E, k = 300001, 8, 2
+    rng = np.random.default_rng(4)
+    x, idx = _inputs(rng, T, E, k)
+    off = np.array([0, 1000, 299000, T])
+    d_w = rng.standard_normal((T, k)).astype(np.float32)
+    st = Step(x, idx, off, None, k, d_w=d_w).run()
+    torch.cuda.synchronize()
+    s = 1 / (1 + np.exp(-x.astype(np.float64)))
+    p = s / s.sum(1, keepdims=True)
+    for q in range(3):
+        a, b = off[q], off[q + 1]
+        assert np.array_equal(st.counts[q].cpu().numpy(), np.bincount(idx[a:b].reshape(-1), minlength=E))
+        want = p[a:b].sum(0)
+        # fp32 sums in blocks: 128 tokens in a chunk, then its 16 chunk groups
+        assert (np.abs(st.prob[q].double().cpu().numpy() - want) <= (2.0 ** -18 + 400 * 2.0 ** -24) * want).all()
+    at = np.unique(np.concatenate([rng.integers(0, T, 300), [0, 999, 1000, 298999, 299000, T - 1]]))
+    counts, coef = st.counts.cpu().numpy(), st.coef.double().cpu().numpy()
+    got = st.d_logits.double().cpu().numpy()
+    for t in at:
+        q = int(np.searchsorted(off, t, side="right") - 1)
+        c = coef[q] * counts[q]
+        si = s[t, idx[t]]
+        ds = (c - (c * p[t]).sum()) / s[t].sum()
+        size = (np.abs(c) + (np.abs(c) * p[t]).sum()) / s[t].sum()
+        np.add.at(ds, idx[t], (d_w[t] - (d_w[t] * si).sum() / si.sum()) / si.sum())
+        np.add.at(size, idx[t], (np.abs(d_w[t]) + (np.abs(d_w[t]) * si).sum() / si.sum()) / si.sum())
+        slope = s[t] * (1 - s[t])
+        assert (np.abs(got[t] - ds * slope) <= 2.0 ** -16 * size * slope).all()
+
+
 def test_with_the_router():
     """moe_route, the balance loss and the gradient together: the weights' term is that of moe_route's own weights."""
     T, H, E, k = 700, 512, 32, 4

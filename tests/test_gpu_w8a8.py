@@ -303,7 +303,8 @@ def _experts_case(T, H, I, E, k, ns, seed):
 
 
 @pytest.mark.parametrize("T,H,I,E,k,ns", [
-    (1, 512, 256, 8, 2, 1), (1, 2048, 512, 16, 4, 0), (9, 1024, 384, 12, 3, 1), (16, 512, 128, 4, 4, 1),
+    (1, 512, 256, 8, 2, 1), (1, 2048, 512, 16, 4, 0), (1, 512, 128, 1, 1, 0), (2, 512, 4096, 8, 8, 0),
+    (2, 1024, 512, 20, 6, 1), (4, 512, 256, 8, 2, 1), (4, 4096, 128, 12, 3, 1), (4, 512, 2048, 9, 8, 1), (9, 1024, 384, 12, 3, 1), (16, 512, 128, 4, 4, 1),
     (17, 512, 256, 8, 2, 1), (64, 1024, 512, 10, 3, 1), (90, 512, 256, 6, 2, 0), (421, 1024, 512, 40, 3, 1),
 ])
 def test_layer_stage_by_stage(T, H, I, E, k, ns):
@@ -376,7 +377,7 @@ def test_full_size_layer(T):
         assert np.array_equal(_f32(y[i:i + 1]), _f32(_scaled(acc, hs[i:i + 1], s2[g].cpu().numpy())))
 
 
-@pytest.mark.parametrize("T", [1, 8, 40, 200])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 8, 40, 200])
 def test_experts_call_is_its_parts(T):
     """moe_w8a8_experts gives the bits of quantise, product, quantise, product, combine."""
     case, layer, _ = _experts_case(T, 1024, 512, 16, 4, 1, 5)
@@ -450,7 +451,7 @@ def test_graph_and_side_stream(T):
         assert float(buf.out.float().abs().max()) > 0
 
 
-def test_binding_refusals():
+def test_binding_refusals(monkeypatch):
     desc = moe.MoeLayerDesc.make(512, 128, 4, 2, 1)
     i8, f, b = (torch.zeros(1 << 17, dtype=t, device="cuda") for t in (torch.int8, torch.float32, torch.bfloat16))
     with pytest.raises(ValueError):
@@ -469,6 +470,10 @@ def test_binding_refusals():
         moe.moe_w8a8_grouped_gemm(desc, 4, i8, f, None, 0, 192, 64, i8, f,
                                   torch.zeros(6, dtype=torch.int32, device="cuda"), moe.MOE_ACT_SWIGLU, b)
     moe.moe_w8a8_gemm(0, 64, 64, i8, f, i8, f, b)                         # nothing to do
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        moe.moe_w8a8_gemm(4, 64, 64, i8, f, i8, f, b)                     # tensors of another device
+    monkeypatch.undo()
     with pytest.raises(ValueError):
         layer = moe.MoELayer(desc, b, f, moe.ExpertWeights(i8, f, i8, f, fmt="int8"))
         layer.forward(b, moe.Buffers(desc, 4))

@@ -145,6 +145,15 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _here(stream, t) -> int:
+    """The stream's handle, after a check that t (one of the call's outputs) is on the current device, where the
+    library launches."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("the tensors are on device %d, the current device is %d"
+                         % (t.get_device(), torch.cuda.current_device()))
+    return _stream(stream)
+
+
 _Tensor = torch.Tensor
 
 
@@ -439,7 +448,7 @@ def moe_fp8_prepack(N: int, K: int, w_canonical, w_packed, stream=None):
 def moe_act_quant_int8(rows: int, K: int, a, codes, scales, stream=None):
     _check("moe_act_quant_int8", lib().moe_act_quant_int8(
         rows, K, _ptr(a, "a", torch.bfloat16, rows * K), _ptr(codes, "codes", torch.int8, rows * K),
-        _ptr(scales, "scales", torch.float32, rows), _stream(stream)))
+        _ptr(scales, "scales", torch.float32, rows), _here(stream, codes)))
 
 
 def moe_w8a8_packed_bytes(n_groups: int, N: int, K: int) -> int:
@@ -455,14 +464,14 @@ def _packed(n_groups: int, N: int, K: int) -> int:
 def moe_w8a8_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stream=None):
     _check("moe_w8a8_prepack", lib().moe_w8a8_prepack(
         n_groups, N, K, _ptr(w_canonical, "w_canonical", torch.int8, n_groups * N * K),
-        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(n_groups, N, K)), _stream(stream)))
+        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(n_groups, N, K)), _here(stream, w_packed)))
 
 
 def moe_w8a8_gemm(M: int, N: int, K: int, a, a_scales, w_packed, w_scales, out, stream=None):
     _check("moe_w8a8_gemm", lib().moe_w8a8_gemm(
         M, N, K, _ptr(a, "a", torch.int8, M * K), _ptr(a_scales, "a_scales", torch.float32, M),
         _ptr(w_packed, "w_packed", torch.int8, _packed(1, N, K)),
-        _ptr(w_scales, "w_scales", torch.float32, N), _ptr(out, "out", torch.bfloat16, M * N), _stream(stream)))
+        _ptr(w_scales, "w_scales", torch.float32, N), _ptr(out, "out", torch.bfloat16, M * N), _here(stream, out)))
 
 
 def moe_w8a8_linear(M: int, N: int, K: int, x, w_packed, w_scales, codes, scales, out, stream=None):
@@ -471,7 +480,7 @@ def moe_w8a8_linear(M: int, N: int, K: int, x, w_packed, w_scales, codes, scales
         M, N, K, _ptr(x, "x", torch.bfloat16, M * K),
         _ptr(w_packed, "w_packed", torch.int8, _packed(1, N, K)),
         _ptr(w_scales, "w_scales", torch.float32, N), _ptr(codes, "codes", torch.int8, M * K),
-        _ptr(scales, "scales", torch.float32, M), _ptr(out, "out", torch.bfloat16, M * N), _stream(stream)))
+        _ptr(scales, "scales", torch.float32, M), _ptr(out, "out", torch.bfloat16, M * N), _here(stream, out)))
 
 
 def moe_w8a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_src: int, N: int, K: int,
@@ -486,7 +495,7 @@ def moe_w8a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_s
         _ptr(w_packed, "w_packed", torch.int8, _packed(G, N, K)),
         _ptr(w_scales, "w_scales", torch.float32, G * N),
         _ptr(group_offsets, "group_offsets", torch.int32, G + 1), act,
-        _ptr(out, "out", torch.bfloat16, R * out_cols), _stream(stream)))
+        _ptr(out, "out", torch.bfloat16, R * out_cols), _here(stream, out)))
 
 
 def moe_w8a8_experts(desc: MoeLayerDesc, T: int, x, topk_w, group_offsets, sorted_token, row_of_slot, w13_packed,
@@ -504,7 +513,7 @@ def moe_w8a8_experts(desc: MoeLayerDesc, T: int, x, topk_w, group_offsets, sorte
         _ptr(w2_scales, "w2_scales", torch.float32, G * H), _ptr(xq, "xq", torch.int8, T * H),
         _ptr(xqs, "xqs", torch.float32, T), _ptr(h, "h", torch.bfloat16, R * I),
         _ptr(hq, "hq", torch.int8, R * I), _ptr(hqs, "hqs", torch.float32, R),
-        _ptr(y, "y", torch.bfloat16, R * H), _ptr(out, "out", torch.bfloat16, T * H), _stream(stream)))
+        _ptr(y, "y", torch.bfloat16, R * H), _ptr(out, "out", torch.bfloat16, T * H), _here(stream, out)))
 
 
 # ------------------------------------------------------------------ router balance and gradient
@@ -521,7 +530,7 @@ def moe_balance_loss(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_
         _ptr(token_mask, "token_mask", torch.uint8, T, optional=True), _ptr(logits, "logits", torch.float32, T * E),
         _ptr(topk_idx, "topk_idx", torch.int32, T * k), alpha, _ptr(counts, "counts", torch.int32, n_seq * E),
         _ptr(prob_sums, "prob_sums", torch.float32, n_seq * E), _ptr(seq_coef, "seq_coef", torch.float32, n_seq),
-        _ptr(loss, "loss", torch.float32, 1), *_ws(ws), _stream(stream)))
+        _ptr(loss, "loss", torch.float32, 1), *_ws(ws), _here(stream, loss)))
 
 
 def moe_route_backward(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_mask, logits, topk_idx, counts,
@@ -535,4 +544,4 @@ def moe_route_backward(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, toke
         _ptr(seq_coef, "seq_coef", torch.float32, n_seq, optional=d_loss is None),
         _ptr(d_loss, "d_loss", torch.float32, 1, optional=True),
         _ptr(d_topk_w, "d_topk_w", torch.float32, T * k, optional=True),
-        _ptr(d_logits, "d_logits", torch.float32, T * E), _stream(stream)))
+        _ptr(d_logits, "d_logits", torch.float32, T * E), _here(stream, d_logits)))

@@ -204,6 +204,10 @@ __global__ __launch_bounds__(256, OCC) void k_w8a8_tiled(Args p) {
         for (int i = 0; i < NS - 1; ++i)
             if (kg + i < KG) step(b[2 * i], b[2 * i + 1], kg + i);
         mfma_drain();
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < NSW; ++j) asm volatile("" : "+v"(acc[c][j]));  // no use before the drain
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no load into LDS outlives the block
 
         // epilogue: the scales, requested before the k loop, go through LDS;
