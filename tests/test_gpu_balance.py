@@ -257,6 +257,24 @@ def test_nothing_is_left_where_it_cancels():
     assert np.linalg.norm(got - grad) <= 1e-6 * np.linalg.norm(grad)
 
 
+def test_scores_near_the_smallest():
+    """Every score of a token near 2^-120 and large upstream gradients: 1 / sum of scores times them passes fp32's range,
+    the gradient itself does not.  At |x| <= 86 the exponential's argument is off by 86 * 1.45 * 2^-24 < 2^-17, a score by
+    less than 2^-16, a gradient of eight such factors by 2^-13 of its terms' sizes."""
+    rng = np.random.default_rng(21)
+    x = -rng.uniform(80, 86, (6, 8)).astype(np.float32)
+    idx = np.stack([rng.permutation(8)[:2] for _ in range(6)])
+    d_w = (rng.standard_normal((6, 2)) * 1e4).astype(np.float32)
+    off = np.array([0, 6])
+    for d_loss, w in ((1e6, None), (None, d_w), (1e6, d_w)):
+        st = Step(x, idx, off, None, 2, d_loss=d_loss, d_w=w).run()
+        torch.cuda.synchronize()
+        ref = _reference(x, idx, off, None, 2, 0.01, 1.0, d_loss, w)
+        got = st.d_logits[:-1].double().cpu().numpy()
+        assert np.isfinite(got).all()
+        assert (np.abs(got - ref[4]) <= 2.0 ** -13 * ref[5]).all()
+
+
 def test_same_bits_every_call():
     rng = np.random.default_rng(7)
     x, idx = _inputs(rng, 9000, 256, 6)

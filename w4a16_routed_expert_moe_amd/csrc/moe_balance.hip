@@ -435,10 +435,12 @@ __device__ __forceinline__ float lane_xor(float v) {
     }
     return v;
 }
-// The routing-weight term of a token, whose choices (score s, gradient g of
-// the weight) sit in eight lanes: (g_j - sum_l g_l s_l / S) / S, written
-// sum_l s_l (g_j - g_l) / S^2 so that nothing cancels (one choice gives 0).
-__device__ __forceinline__ float weight_term(float s, float g) {
+// The routing-weight term of a token's gradient, whose choices (score s, its
+// slope, gradient g of the weight) sit in eight lanes:
+// (g_j - sum_l g_l s_l / S) / S slope_j, written
+// (sum_l s_l (g_j - g_l) / S) (slope_j / S) so that nothing cancels (one choice
+// gives 0) and nothing overflows where every score is tiny (slope <= s <= S).
+__device__ __forceinline__ float weight_term(float s, float slope, float g) {
     float S = s, d = 0.0f;
 #define MOE_PAIR(X)                                \
     {                                                             \
@@ -449,7 +451,7 @@ __device__ __forceinline__ float weight_term(float s, float g) {
     MOE_PAIR(1) MOE_PAIR(2) MOE_PAIR(3) MOE_PAIR(4) MOE_PAIR(5) MOE_PAIR(6) MOE_PAIR(7)
 #undef MOE_PAIR
     const float r = S == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(S);
-    return d * r * r;
+    return (d * r) * (r * slope);
 }
 
 // A wave takes TW consecutive tokens, U of them at a time (1, or 8: the
@@ -521,8 +523,9 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
         if ((unsigned)ek >= (unsigned)E) ek = -1;
         if (d_w) {
             if (ek >= 0) xk = logits[(size_t)(tb + lu) * E + ek];
-            const float sk = ek >= 0 ? score(xk) : 0.0f;
-            const float term_k = weight_term(sk, dw);
+            float slope_k;
+            const float sk = score(xk, slope_k);
+            const float term_k = weight_term(ek >= 0 ? sk : 0.0f, slope_k, dw);
             // (the same index twice in a row: its terms add)
             if (ek >= 0) atomicAdd(&term[lu < U ? lu : 0][ek], scale * term_k);
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -564,11 +567,11 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
                 const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
                 const float mean = cs * inv;
 #pragma unroll
-                for (int i = 0; i < kSlots; ++i) ds[i] = __builtin_fmaf(c[i] - mean, inv, ds[i]);
+                for (int i = 0; i < kSlots; ++i) ds[i] = __builtin_fmaf(c[i] - mean, slope[i] * inv, ds[i]);
             }
             float *row = d_logits + (size_t)t * E;
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i) ds[i] = live ? ds[i] * slope[i] : 0.0f;
+            for (int i = 0; i < kSlots; ++i) ds[i] = live ? ds[i] : 0.0f;
             if (VEC) {
                 if (4 * l < E) *(float4 *)(row + 4 * l) = float4{ds[0], ds[1], ds[2], ds[3]};
             } else {
