@@ -257,6 +257,17 @@ def test_nothing_is_left_where_it_cancels():
     assert np.linalg.norm(got - grad) <= 1e-6 * np.linalg.norm(grad)
 
 
+@pytest.mark.parametrize("T", [700, 9001])
+def test_runs_of_empty_sequences(T):
+    """Thousands of empty sequences before, between and behind those that hold tokens."""
+    rng = np.random.default_rng(T)
+    x, idx = _inputs(rng, T, 20, 3)
+    cuts = np.sort(rng.integers(0, T + 1, 5))
+    off = np.concatenate([[0] * 1000] + [[c] * n for c, n in zip(cuts, (1, 3000, 2, 700, 64))] + [[T] * 900])
+    st = Step(x, idx, off, None, 3, d_w=rng.standard_normal((T, 3)).astype(np.float32)).run()
+    _check(st, _reference(x, idx, off, None, 3, 0.01, 1.0, 1.0, st.d_w.cpu().numpy()), T)
+
+
 def test_scores_near_the_smallest():
     """Every score of a token near 2^-120 and large upstream gradients: 1 / sum of scores times them passes fp32's range,
     the gradient itself does not.  At |x| <= 86 the exponential's argument is off by 86 * 1.45 * 2^-24 < 2^-17, a score by

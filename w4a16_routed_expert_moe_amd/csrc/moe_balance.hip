@@ -245,7 +245,10 @@ __global__ __launch_bounds__(64 * W) void k_balance_part(Seqs q, const float *__
     for (int s = seq_of(q, t0); s < q.n; ++s) {
         const int begin = seq_begin(q, s), a = max(begin, t0), b = min(seq_end(q, s), t1);
         if (begin >= t1) break;
-        if (a >= b) continue;
+        if (a >= b) {  // empty, and any number after it: on to the one that holds token a
+            s = max(s, seq_of(q, a) - 1);
+            continue;
+        }
         float prob;
         int cnt, live;
         tok.segment(t0, a, b, sh, buf, prob, cnt, live);
@@ -536,9 +539,13 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
         for (int u = 0; u < U; ++u) {
             const int t = tb + u;
             if (t >= t1) break;
-            while (s < q.n && t >= end) {
+            if (s < q.n && t >= end) {
                 ++s;
                 enter();
+                if (s < q.n && t >= end) {  // empty, and any number after it
+                    s = max(s + 1, seq_of(q, t));
+                    enter();
+                }
             }
             const bool live = on[u] && s < q.n && t >= begin;
             float slope[kSlots], sum = 0.0f, cs = 0.0f, ds[kSlots] = {0.f, 0.f, 0.f, 0.f};
