@@ -469,6 +469,7 @@ moe_status moe_fp8_prepack(int32_t N, int32_t K, const uint8_t *w_canonical, uin
 /*   out[m][n] = bf16( acc * a_scales[m] * w_scales[n] )                     */
 /* The sum is exact whatever its order, so the dense, the grouped and the    */
 /* one-launch forms give the same bits for the same codes and scales.        */
+/* Outputs and scratch overlap neither each other nor an input.              */
 
 /* Quantisation of each row by itself, symmetric: with amax = max |a[r][k]|  */
 /*   scales[r]   = amax / 127 (fp32, rounded to nearest)                     */
@@ -596,6 +597,7 @@ moe_status moe_w8a8_experts(const moe_layer_desc *desc, int32_t T, const uint16_
 /*                bytes, 16-byte aligned, zero before the first call (every  */
 /*                call leaves its counter zero); calls that may overlap in   */
 /*                time need distinct workspaces                              */
+/* Outputs, here and below, overlap neither each other nor an input.         */
 /* Of desc only n_routed and top_k matter here (and routed_scale below).     */
 size_t moe_balance_workspace_bytes(const moe_layer_desc *desc, int32_t T, int32_t n_seq);
 moe_status moe_balance_loss(const moe_layer_desc *desc, int32_t T, int32_t n_seq,

@@ -137,6 +137,40 @@ def test_prepack_layout(G, N, K):
     assert np.array_equal(got.cpu().numpy(), _packed_ref(w))
 
 
+def test_layout_and_quantisation_past_32_bit_threads():
+    """Sizes whose pieces, and whose rows times 1024 threads, pass 2^32 in one call."""
+    G, N, K = 9, 65536, 65536
+    rng = np.random.default_rng(11)
+    w = torch.zeros((G, N, K), dtype=torch.int8, device="cuda")
+    at = [(0, 64, 128), (3, N - 64, 0), (7, N - 64, K - 128), (8, 0, 0), (8, N - 64, K - 128)]
+    parts = [rng.integers(-128, 128, (1, 64, 128), dtype=np.int8) for _ in at]
+    for (g, n, k), part in zip(at, parts):
+        w[g, n:n + 64, k:k + 128] = torch.from_numpy(part[0]).cuda()
+    out = torch.empty(moe.moe_w8a8_packed_bytes(G, N, K), dtype=torch.int8, device="cuda")
+    moe.moe_w8a8_prepack(G, N, K, w, out)
+    blocks = out.view(G, N // 16, K // 64, 1024)
+    for (g, n, k), part in zip(at, parts):
+        got = blocks[g, n // 16:n // 16 + 4, k // 64:k // 64 + 2].cpu().numpy()
+        assert np.array_equal(got.reshape(-1), _packed_ref(part)), (g, n, k)
+    del w, out, blocks
+    torch.cuda.empty_cache()
+    rows, K = (1 << 22) + 3, 16400
+    x = torch.zeros((rows, K), dtype=torch.bfloat16, device="cuda")
+    at = [0, (1 << 21) - 1, 1 << 21, rows - 4, rows - 1]
+    part = _rows(rng, len(at), K, 10.0)
+    for i, r in enumerate(at):
+        x[r] = to_dev_bf16(part[i:i + 1])[0]
+    codes = torch.empty((rows, K), dtype=torch.int8, device="cuda")
+    scales = torch.empty(rows, device="cuda")
+    moe.moe_act_quant_int8(rows, K, x, codes, scales)
+    torch.cuda.synchronize()
+    rc, rs = _quant_ref(part)
+    assert np.array_equal(codes[at].cpu().numpy(), rc) and np.array_equal(scales[at].cpu().numpy(), rs)
+    assert int((scales != 0).sum()) == len(at)
+    del x, codes
+    torch.cuda.empty_cache()
+
+
 def _int_product(a, w):
     """int64 sums of int8 codes (fp64 holds every partial sum exactly)."""
     return (a.astype(np.float64) @ w.astype(np.float64).T).astype(np.int64)

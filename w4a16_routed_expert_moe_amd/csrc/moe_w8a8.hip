@@ -10,6 +10,8 @@
 // |a| <= 127 and |w| <= 128, so the sum stays below 2^31 up to K = 65536 and
 // its order does not matter: every kernel and every split of K gives the same
 // bits.
+#include <algorithm>
+
 #include "moe_route_common.h"
 #include "moe_w8a8.h"
 
@@ -91,20 +93,15 @@ void launch_quant(int rows, int K, const uint16_t *a, int8_t *codes, float *scal
 }
 
 // ---------------------------------------------------------------- prepack
-__global__ void k_w8a8_prepack(const int8_t *__restrict__ src, int8_t *__restrict__ dst, int G, int N, int K, int NT,
-                               int KB) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;  // one 16-byte piece each
-    const long long total = (long long)G * NT * KB * 64;
+// One 16-byte piece per thread, a group per blockIdx.y.
+__global__ void k_w8a8_prepack(const int8_t *__restrict__ src, int8_t *__restrict__ dst, int N, int K, int NT, int KB) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x, total = NT * KB * 64, g = blockIdx.y;
     if (i >= total) return;
-    const int lane = (int)(i & 63);
-    const long long blk = i >> 6;
-    const int kb = (int)(blk % KB);
-    const long long gt = blk / KB;
-    const int t = (int)(gt % NT), g = (int)(gt / NT);
+    const int lane = i & 63, blk = i >> 6, kb = blk % KB, t = blk / KB;
     const int n = packed_row(t, lane & 15), k = 64 * kb + 16 * (lane >> 4);
     u32x4 v = u32x4{0u, 0u, 0u, 0u};
     if (n < N && k < K) v = *(const u32x4 *)(src + ((size_t)g * N + n) * K + k);
-    *(u32x4 *)(dst + 16 * i) = v;
+    *(u32x4 *)(dst + 16 * ((size_t)g * total + i)) = v;
 }
 
 // ---------------------------------------------------------------- weight stream
@@ -481,8 +478,13 @@ extern "C" moe_status moe_act_quant_int8(int32_t rows, int32_t K, const uint16_t
     if (rows == 0) return MOE_OK;
     if (!a || !codes || !scales) return MOE_ERR_NULL;
     if (!aligned(a, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
-    w8::launch_quant(rows, K, a, codes, scales, (hipStream_t)stream);
-    return launch_status();
+    constexpr int most = 1 << 21;  // of 1024 threads a row: fewer than 2^32 in a launch
+    for (int r = 0; r < rows; r += most) {
+        w8::launch_quant(std::min(most, rows - r), K, a + (size_t)r * K, codes + (size_t)r * K, scales + r,
+                         (hipStream_t)stream);
+        MOE_TRY(launch_status());
+    }
+    return MOE_OK;
 }
 
 extern "C" size_t moe_w8a8_packed_bytes(int32_t n_groups, int32_t N, int32_t K) {
@@ -498,11 +500,16 @@ extern "C" moe_status moe_w8a8_prepack(int32_t n_groups, int32_t N, int32_t K, c
     if (!aligned(w_canonical, 16) || !aligned(w_packed, 16)) return MOE_ERR_ALIGN;
     const uintptr_t s0 = (uintptr_t)w_canonical, d0 = (uintptr_t)w_packed;
     if (s0 < d0 + bytes && d0 < s0 + (size_t)n_groups * N * K) return MOE_ERR_SHAPE;  // overlapping buffers
-    const size_t pieces = bytes / 16;
-    if ((pieces + 255) / 256 > 0x7FFFFFFF) return MOE_ERR_SHAPE;
-    hipLaunchKernelGGL(w8::k_w8a8_prepack, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, (hipStream_t)stream,
-                       w_canonical, w_packed, n_groups, N, K, w8::subtiles(N), w8::kblocks(K));
-    return launch_status();
+    // up to 2^31 threads in a launch (a group has at most 2^28)
+    const size_t pieces = bytes / 16 / n_groups, out = bytes / n_groups;
+    const int most = (int)std::min<size_t>(n_groups, ((size_t)1 << 31) / pieces);
+    for (int g = 0; g < n_groups; g += most) {
+        hipLaunchKernelGGL(w8::k_w8a8_prepack, dim3((unsigned)((pieces + 255) / 256), std::min(most, n_groups - g)),
+                           dim3(256), 0, (hipStream_t)stream, w_canonical + (size_t)g * N * K, w_packed + g * out, N, K,
+                           w8::subtiles(N), w8::kblocks(K));
+        MOE_TRY(launch_status());
+    }
+    return MOE_OK;
 }
 
 extern "C" moe_status moe_w8a8_gemm(int32_t M, int32_t N, int32_t K, const int8_t *a, const float *a_scales,
