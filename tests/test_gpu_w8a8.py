@@ -511,3 +511,30 @@ def test_binding_refusals(monkeypatch):
     with pytest.raises(ValueError):
         layer = moe.MoELayer(desc, b, f, moe.ExpertWeights(i8, f, i8, f, fmt="int8"))
         layer.forward(b, moe.Buffers(desc, 4))
+
+
+def test_every_tensor_is_on_the_current_device():
+    """Each tensor of each call, one at a time, on another device than the rest: refused."""
+    class Away(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    n = 1 << 18
+    t = {k: torch.zeros(n, dtype=v, device="cuda") for k, v in
+         dict(b=torch.bfloat16, f=torch.float32, i=torch.int32, c=torch.int8, u=torch.uint8).items()}
+    desc = moe.MoeLayerDesc.make(128, 128, 4, 2, 1)
+    for fn, args in ((moe.moe_act_quant_int8, [4, 64, "b", "c", "f"]),
+                     (moe.moe_w8a8_prepack, [1, 64, 128, "c", "c"]),
+                     (moe.moe_w8a8_gemm, [4, 64, 128, "c", "f", "c", "f", "b"]),
+                     (moe.moe_w8a8_linear, [4, 64, 128, "b", "c", "f", "c", "f", "b"]),
+                     (moe.moe_w8a8_grouped_gemm, [desc, 2, "c", "f", "i", 2, 128, 128, "c", "f", "i", 0, "b"]),
+                     (moe.moe_w8a8_experts, [desc, 1, "b", "f", "i", "i", "i", "c", "f", "c", "f", "c", "f", "b", "c",
+                                             "f", "b", "b"]),
+                     (moe.moe_balance_loss, [desc, 4, 1, "i", "u", "f", "i", 0.1, "i", "f", "f", "f", "u"]),
+                     (moe.moe_route_backward, [desc, 4, 1, "i", "u", "f", "i", "i", "f", "f", "f", "f"])):
+        for at, a in enumerate(args):
+            if isinstance(a, str):
+                call = [t[x] if isinstance(x, str) else x for x in args]
+                call[at] = call[at].as_subclass(Away)
+                with pytest.raises(ValueError, match="device"):
+                    fn(*call)

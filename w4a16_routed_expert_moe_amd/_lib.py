@@ -137,21 +137,12 @@ def _check(fn: str, status: int):
         raise MoeError(fn, status, lib().moe_status_str(status).decode())
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev=None) -> int:
     if stream is None:  # the current stream's handle, without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
     return int(stream)
-
-
-def _here(stream, t) -> int:
-    """The stream's handle, after a check that t (one of the call's outputs) is on the current device, where the
-    library launches."""
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError("the tensors are on device %d, the current device is %d"
-                         % (t.get_device(), torch.cuda.current_device()))
-    return _stream(stream)
 
 
 _Tensor = torch.Tensor
@@ -173,6 +164,19 @@ def _ptr(t, name, dtype, numel, optional=False):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     raise ValueError("%s holds %d elements, needs %d" % (name, t.numel(), numel))
+
+
+_BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
+
+
+def _at(dev, t, name, dtype, numel, optional=False):
+    """_ptr of a tensor that has to be on device dev: the current one, where the library launches."""
+    if isinstance(t, _Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    p = _ptr(t, name, dtype, numel, optional)
+    if p is not None:
+        raise ValueError("%s is on device %d, the current device is %d" % (name, t.get_device(), dev))
+    return p
 
 
 # ------------------------------------------------------------------ entry points
@@ -446,9 +450,10 @@ def moe_fp8_prepack(N: int, K: int, w_canonical, w_packed, stream=None):
 
 # ------------------------------------------------------------------ W8A8
 def moe_act_quant_int8(rows: int, K: int, a, codes, scales, stream=None):
+    d = torch.cuda.current_device()
     _check("moe_act_quant_int8", lib().moe_act_quant_int8(
-        rows, K, _ptr(a, "a", torch.bfloat16, rows * K), _ptr(codes, "codes", torch.int8, rows * K),
-        _ptr(scales, "scales", torch.float32, rows), _here(stream, codes)))
+        rows, K, _at(d, a, "a", _BF16, rows * K), _at(d, codes, "codes", _I8, rows * K),
+        _at(d, scales, "scales", _F32, rows), _stream(stream, d)))
 
 
 def moe_w8a8_packed_bytes(n_groups: int, N: int, K: int) -> int:
@@ -462,25 +467,28 @@ def _packed(n_groups: int, N: int, K: int) -> int:
 
 
 def moe_w8a8_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stream=None):
+    d = torch.cuda.current_device()
     _check("moe_w8a8_prepack", lib().moe_w8a8_prepack(
-        n_groups, N, K, _ptr(w_canonical, "w_canonical", torch.int8, n_groups * N * K),
-        _ptr(w_packed, "w_packed", torch.int8, moe_w8a8_packed_bytes(n_groups, N, K)), _here(stream, w_packed)))
+        n_groups, N, K, _at(d, w_canonical, "w_canonical", _I8, n_groups * N * K),
+        _at(d, w_packed, "w_packed", _I8, moe_w8a8_packed_bytes(n_groups, N, K)), _stream(stream, d)))
 
 
 def moe_w8a8_gemm(M: int, N: int, K: int, a, a_scales, w_packed, w_scales, out, stream=None):
+    d = torch.cuda.current_device()
     _check("moe_w8a8_gemm", lib().moe_w8a8_gemm(
-        M, N, K, _ptr(a, "a", torch.int8, M * K), _ptr(a_scales, "a_scales", torch.float32, M),
-        _ptr(w_packed, "w_packed", torch.int8, _packed(1, N, K)),
-        _ptr(w_scales, "w_scales", torch.float32, N), _ptr(out, "out", torch.bfloat16, M * N), _here(stream, out)))
+        M, N, K, _at(d, a, "a", _I8, M * K), _at(d, a_scales, "a_scales", _F32, M),
+        _at(d, w_packed, "w_packed", _I8, _packed(1, N, K)),
+        _at(d, w_scales, "w_scales", _F32, N), _at(d, out, "out", _BF16, M * N), _stream(stream, d)))
 
 
 def moe_w8a8_linear(M: int, N: int, K: int, x, w_packed, w_scales, codes, scales, out, stream=None):
     """moe_act_quant_int8 + moe_w8a8_gemm in one call; codes and scales are scratch."""
+    d = torch.cuda.current_device()
     _check("moe_w8a8_linear", lib().moe_w8a8_linear(
-        M, N, K, _ptr(x, "x", torch.bfloat16, M * K),
-        _ptr(w_packed, "w_packed", torch.int8, _packed(1, N, K)),
-        _ptr(w_scales, "w_scales", torch.float32, N), _ptr(codes, "codes", torch.int8, M * K),
-        _ptr(scales, "scales", torch.float32, M), _ptr(out, "out", torch.bfloat16, M * N), _here(stream, out)))
+        M, N, K, _at(d, x, "x", _BF16, M * K),
+        _at(d, w_packed, "w_packed", _I8, _packed(1, N, K)),
+        _at(d, w_scales, "w_scales", _F32, N), _at(d, codes, "codes", _I8, M * K),
+        _at(d, scales, "scales", _F32, M), _at(d, out, "out", _BF16, M * N), _stream(stream, d)))
 
 
 def moe_w8a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_src: int, N: int, K: int,
@@ -488,32 +496,34 @@ def moe_w8a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_s
     G, R = desc.groups, desc.rows(T)
     a_rows = n_src if a_gather is not None else R
     out_cols = N // 2 if act == MOE_ACT_SWIGLU else N
+    d = torch.cuda.current_device()
     _check("moe_w8a8_grouped_gemm", lib().moe_w8a8_grouped_gemm(
-        ctypes.byref(desc), T, _ptr(a, "a", torch.int8, a_rows * K),
-        _ptr(a_scales, "a_scales", torch.float32, a_rows),
-        _ptr(a_gather, "a_gather", torch.int32, R, optional=True), n_src, N, K,
-        _ptr(w_packed, "w_packed", torch.int8, _packed(G, N, K)),
-        _ptr(w_scales, "w_scales", torch.float32, G * N),
-        _ptr(group_offsets, "group_offsets", torch.int32, G + 1), act,
-        _ptr(out, "out", torch.bfloat16, R * out_cols), _here(stream, out)))
+        ctypes.byref(desc), T, _at(d, a, "a", _I8, a_rows * K),
+        _at(d, a_scales, "a_scales", _F32, a_rows),
+        _at(d, a_gather, "a_gather", _I32, R, optional=True), n_src, N, K,
+        _at(d, w_packed, "w_packed", _I8, _packed(G, N, K)),
+        _at(d, w_scales, "w_scales", _F32, G * N),
+        _at(d, group_offsets, "group_offsets", _I32, G + 1), act,
+        _at(d, out, "out", _BF16, R * out_cols), _stream(stream, d)))
 
 
 def moe_w8a8_experts(desc: MoeLayerDesc, T: int, x, topk_w, group_offsets, sorted_token, row_of_slot, w13_packed,
                      w13_scales, w2_packed, w2_scales, xq, xqs, h, hq, hqs, y, out, stream=None):
     """Everything after the routing for INT8 experts; xq, xqs, hq and hqs are scratch."""
     H, I, G, R, S = desc.hidden, desc.inter, desc.groups, desc.rows(T), desc.top_k + desc.n_shared
+    d = torch.cuda.current_device()
     _check("moe_w8a8_experts", lib().moe_w8a8_experts(
-        ctypes.byref(desc), T, _ptr(x, "x", torch.bfloat16, T * H),
-        _ptr(topk_w, "topk_w", torch.float32, T * desc.top_k),
-        _ptr(group_offsets, "group_offsets", torch.int32, G + 1),
-        _ptr(sorted_token, "sorted_token", torch.int32, R), _ptr(row_of_slot, "row_of_slot", torch.int32, T * S),
-        _ptr(w13_packed, "w13_packed", torch.int8, _packed(G, 2 * I, H)),
-        _ptr(w13_scales, "w13_scales", torch.float32, G * 2 * I),
-        _ptr(w2_packed, "w2_packed", torch.int8, _packed(G, H, I)),
-        _ptr(w2_scales, "w2_scales", torch.float32, G * H), _ptr(xq, "xq", torch.int8, T * H),
-        _ptr(xqs, "xqs", torch.float32, T), _ptr(h, "h", torch.bfloat16, R * I),
-        _ptr(hq, "hq", torch.int8, R * I), _ptr(hqs, "hqs", torch.float32, R),
-        _ptr(y, "y", torch.bfloat16, R * H), _ptr(out, "out", torch.bfloat16, T * H), _here(stream, out)))
+        ctypes.byref(desc), T, _at(d, x, "x", _BF16, T * H),
+        _at(d, topk_w, "topk_w", _F32, T * desc.top_k),
+        _at(d, group_offsets, "group_offsets", _I32, G + 1),
+        _at(d, sorted_token, "sorted_token", _I32, R), _at(d, row_of_slot, "row_of_slot", _I32, T * S),
+        _at(d, w13_packed, "w13_packed", _I8, _packed(G, 2 * I, H)),
+        _at(d, w13_scales, "w13_scales", _F32, G * 2 * I),
+        _at(d, w2_packed, "w2_packed", _I8, _packed(G, H, I)),
+        _at(d, w2_scales, "w2_scales", _F32, G * H), _at(d, xq, "xq", _I8, T * H),
+        _at(d, xqs, "xqs", _F32, T), _at(d, h, "h", _BF16, R * I),
+        _at(d, hq, "hq", _I8, R * I), _at(d, hqs, "hqs", _F32, R),
+        _at(d, y, "y", _BF16, R * H), _at(d, out, "out", _BF16, T * H), _stream(stream, d)))
 
 
 # ------------------------------------------------------------------ router balance and gradient
@@ -525,23 +535,25 @@ def moe_balance_workspace_bytes(desc: MoeLayerDesc, T: int, n_seq: int) -> int:
 def moe_balance_loss(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_mask, logits, topk_idx, alpha: float,
                      counts, prob_sums, seq_coef, loss, ws, stream=None):
     E, k = desc.n_routed, desc.top_k
+    d = torch.cuda.current_device()
     _check("moe_balance_loss", lib().moe_balance_loss(
-        ctypes.byref(desc), T, n_seq, _ptr(seq_offsets, "seq_offsets", torch.int32, n_seq + 1, optional=True),
-        _ptr(token_mask, "token_mask", torch.uint8, T, optional=True), _ptr(logits, "logits", torch.float32, T * E),
-        _ptr(topk_idx, "topk_idx", torch.int32, T * k), alpha, _ptr(counts, "counts", torch.int32, n_seq * E),
-        _ptr(prob_sums, "prob_sums", torch.float32, n_seq * E), _ptr(seq_coef, "seq_coef", torch.float32, n_seq),
-        _ptr(loss, "loss", torch.float32, 1), *_ws(ws), _here(stream, loss)))
+        ctypes.byref(desc), T, n_seq, _at(d, seq_offsets, "seq_offsets", _I32, n_seq + 1, optional=True),
+        _at(d, token_mask, "token_mask", _U8, T, optional=True), _at(d, logits, "logits", _F32, T * E),
+        _at(d, topk_idx, "topk_idx", _I32, T * k), alpha, _at(d, counts, "counts", _I32, n_seq * E),
+        _at(d, prob_sums, "prob_sums", _F32, n_seq * E), _at(d, seq_coef, "seq_coef", _F32, n_seq),
+        _at(d, loss, "loss", _F32, 1), _at(d, ws, "ws", _U8, 0), ws.numel(), _stream(stream, d)))
 
 
 def moe_route_backward(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_mask, logits, topk_idx, counts,
                        seq_coef, d_loss, d_topk_w, d_logits, stream=None):
     E, k = desc.n_routed, desc.top_k
+    d = torch.cuda.current_device()
     _check("moe_route_backward", lib().moe_route_backward(
-        ctypes.byref(desc), T, n_seq, _ptr(seq_offsets, "seq_offsets", torch.int32, n_seq + 1, optional=True),
-        _ptr(token_mask, "token_mask", torch.uint8, T, optional=True), _ptr(logits, "logits", torch.float32, T * E),
-        _ptr(topk_idx, "topk_idx", torch.int32, T * k),
-        _ptr(counts, "counts", torch.int32, n_seq * E, optional=d_loss is None),
-        _ptr(seq_coef, "seq_coef", torch.float32, n_seq, optional=d_loss is None),
-        _ptr(d_loss, "d_loss", torch.float32, 1, optional=True),
-        _ptr(d_topk_w, "d_topk_w", torch.float32, T * k, optional=True),
-        _ptr(d_logits, "d_logits", torch.float32, T * E), _here(stream, d_logits)))
+        ctypes.byref(desc), T, n_seq, _at(d, seq_offsets, "seq_offsets", _I32, n_seq + 1, optional=True),
+        _at(d, token_mask, "token_mask", _U8, T, optional=True), _at(d, logits, "logits", _F32, T * E),
+        _at(d, topk_idx, "topk_idx", _I32, T * k),
+        _at(d, counts, "counts", _I32, n_seq * E, optional=d_loss is None),
+        _at(d, seq_coef, "seq_coef", _F32, n_seq, optional=d_loss is None),
+        _at(d, d_loss, "d_loss", _F32, 1, optional=True),
+        _at(d, d_topk_w, "d_topk_w", _F32, T * k, optional=True),
+        _at(d, d_logits, "d_logits", _F32, T * E), _stream(stream, d)))
