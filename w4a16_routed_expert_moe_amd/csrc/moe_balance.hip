@@ -7,9 +7,11 @@
 //   coef[q] = alpha E / (k n_q^2 Q')
 //
 // The loss reads every logit once and the gradient reads and writes every
-// one once: both are bound by HBM (at 65536 x 256: 67 MB and 134 MB).  A wave
-// takes a token; a lane holds four experts, so the sum over a token's experts
-// is one wave reduction and the sums over tokens stay in registers.
+// one once: at 65536 x 256, 67 MB in 23 to 28 us plus 6 us for the sums of the
+// chunks, and 134 MB in 27 to 29 us (4.9 TB/s, a copy's rate).  Up to 8192
+// tokens both are bound by latency: 4 to 7 us a launch.  A wave takes a token;
+// a lane holds four experts, so the sum over a token's experts is one wave
+// reduction and the sums over tokens stay in registers.
 #include "moe_route_common.h"
 
 namespace moe {
@@ -17,8 +19,12 @@ namespace {
 
 constexpr int kSlots = 4;          // experts per lane: E <= 256
 constexpr int kMaxExperts = kSlots * kWave;
-constexpr int kOneTokens = 128;    // up to here the loss is one workgroup's work, one launch
-constexpr int kOneSeqs = 64;
+// Up to here the loss is one workgroup's work, one launch: about 0.8 us per
+// sequence.  Loss + gradient of 33 tokens of 256 experts, us, against two
+// launches for the loss: 1 sequence 8.1 / 10.9, 4 10.4 / 11.6, 8 13.5 / 12.4,
+// 32 32.6 / 15.5; of 128 tokens 11.0 / 11.2, 13.3 / 11.4, 16.6 / 12.6.  Called
+// one by one, the host's 14 to 15 with one launch and 17.5 with two count.
+constexpr int kOneTokens = 128, kOneSeqs = 6;
 constexpr int kChunks = 256;       // token chunks of the partial sums: one per CU ...
 constexpr int kMinChunk = 8, kMaxChunk = 128;  // ... of at least 8 tokens and at most as many as fit the registers
 
@@ -382,47 +388,50 @@ __global__ __launch_bounds__(64 * GR) void k_balance_reduce(Seqs q, int E, int k
     if (tid == 0) *o.loss = (float)sum;
 }
 
-// Few tokens and sequences: everything in one workgroup, in one launch.
+// Few tokens and sequences: everything in one workgroup, in one launch.  The
+// sequences' bounds are read once; a thread adds its expert's products over
+// the sequences, divided by n_q^2, and one reduction at the end gives the loss.
 template <bool VEC, int U>
 __global__ __launch_bounds__(1024) void k_balance_one(Seqs q, const float *__restrict__ logits,
                                                       const int32_t *__restrict__ idx, int E, int k, float alpha,
                                                       Out o) {
     constexpr int W = 16;
     __shared__ __attribute__((aligned(16))) SegmentLds<W> sh;
-    __shared__ double sdot[kOneSeqs][4];
-    __shared__ int snq[kOneSeqs];
+    __shared__ double sdot[4];
+    __shared__ int snq[kOneSeqs], sbegin[kOneSeqs], send[kOneSeqs];
     const int tid = threadIdx.x;
     if (tid < kMaxExperts) sh.hist[0][tid] = sh.hist[1][tid] = 0;
+    if (tid < q.n) {
+        sbegin[tid] = seq_begin(q, tid);
+        send[tid] = seq_end(q, tid);
+    }
     Tokens<VEC, W, U> tok;
     tok.load(q, logits, idx, E, k, 0, q.T);
     __syncthreads();
+    double dot = 0.0;
     for (int s = 0; s < q.n; ++s) {
         float prob;
         int cnt, live;
-        tok.segment(0, seq_begin(q, s), seq_end(q, s), sh, s & 1, prob, cnt, live);
-        if (tid < kMaxExperts) {
-            double dot = 0.0;
-            if (tid < E) {
-                o.counts[(size_t)s * E + tid] = cnt;
-                o.prob[(size_t)s * E + tid] = prob;
-                dot = (double)cnt * (double)prob;
-            }
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d, kWave);
-            if (lane_id() == 0) sdot[s][tid >> 6] = dot;
-            if (tid == 0) snq[s] = live;
+        tok.segment(0, sbegin[s], send[s], sh, s & 1, prob, cnt, live);
+        if (tid < E) {
+            o.counts[(size_t)s * E + tid] = cnt;
+            o.prob[(size_t)s * E + tid] = prob;
+            if (live) dot += (double)cnt * (double)prob / ((double)live * live);
         }
+        if (tid == 0) snq[s] = live;
+    }
+    if (tid < kMaxExperts) {
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d, kWave);
+        if (lane_id() == 0) sdot[tid >> 6] = dot;
     }
     __syncthreads();
     if (tid < kWave) {
         const int n = tid < q.n ? snq[tid] : 0;
         const int some = __popcll(__ballot(n > 0));
-        const double c = coef_of(alpha, E, k, n, some);
-        if (tid < q.n) o.coef[tid] = (float)c;
-        double sum = n > 0 && c != 0.0 ? c * (((sdot[tid][0] + sdot[tid][1]) + sdot[tid][2]) + sdot[tid][3]) : 0.0;
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, kWave);
-        if (tid == 0) *o.loss = (float)sum;
+        if (tid < q.n) o.coef[tid] = (float)coef_of(alpha, E, k, n, some);
+        const double c = coef_of(alpha, E, k, 1, some), sum = ((sdot[0] + sdot[1]) + sdot[2]) + sdot[3];
+        if (tid == 0) *o.loss = some && c != 0.0 ? (float)(c * sum) : 0.0f;
     }
 }
 

@@ -8,16 +8,19 @@
 // workgroup share, go from global memory into registers, PF half steps (64 k)
 // ahead, so that per matrix instruction of 16 cycles only 1024 / NSW bytes
 // come out of LDS.  ONCE: groups of one tile, whose weights are read by one
-// workgroup and not kept in the caches.  The sums are exact in int32, so the k loop holds nothing
-// but loads and matrix instructions; both scales are applied in the epilogue.
+// workgroup and not kept in the caches.  The sums are exact in int32, so the
+// k loop holds nothing but loads and matrix instructions; both scales are
+// applied in the epilogue.
 // The wave multiplies only the m-tiles (16 rows) that have rows: the count is
 // a constant of each instance of the k loop, chosen once per work item.
 //
-// What bounds it.  Many rows: power.  The matrix instruction alone, on random
-// bytes, runs at 3800 TOPS here (4950 on zeros); a dense 8192 x 4096 x 4096
-// product takes 115 to 120 us (2300 to 2400 TOPS), and the same k loop
-// without its loads 93.  Few rows per group: the weights' bytes (the layer's
-// experts at 512 tokens: 5.8 TB/s).
+// What bounds it.  Dense with many rows: power.  The matrix instruction alone,
+// on random bytes, runs at 3800 TOPS here (4830 on zeros); an 8192 x 4096 x
+// 4096 product takes 113 to 134 us (2050 to 2430 TOPS) at 2.03 GHz with the
+// matrix units busy 57% of the time, and the same k loop without its loads 90.
+// Groups of 200 rows (the layer's experts at 8192 tokens): HBM, 4.96 GB read
+// and 0.24 written in 1.04 ms and 2.5 + 0.47 GB in 0.60 ms, 5.0 TB/s, a copy's
+// rate.  Few rows per group: the weights' bytes (64 tokens: 6.6 TB/s read).
 #include <algorithm>
 #include <type_traits>
 
