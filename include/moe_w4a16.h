@@ -512,8 +512,8 @@ moe_status moe_w8a8_gemm(int32_t M, int32_t N, int32_t K, const int8_t *a, const
                          void *stream);
 
 /* moe_act_quant_int8 followed by moe_w8a8_gemm, with the same bits in out;  */
-/* up to 4 rows with K <= 4096 it is one launch, which quantises each row    */
-/* where it is used.                                                         */
+/* few rows (up to 4, and up to 16 short ones) with K <= 4096 are one launch, */
+/* which quantises each row where it is used.                                */
 /*   x          bf16 [M][K], 16-byte aligned                                 */
 /*   codes, scales  scratch: int8 [M][K] (16-byte aligned) and fp32 [M];     */
 /*              their contents afterwards are unspecified (calls that may    */
@@ -543,9 +543,9 @@ moe_status moe_w8a8_grouped_gemm(const moe_layer_desc *desc, int32_t T, const in
 /* Everything after the routing for experts in INT8, in one call: quantise   */
 /* x, gate/up product with SwiGLU into h, quantise h, down product into y,   */
 /* moe_combine into out.  The same bits as those calls one after the other   */
-/* (up to 4 tokens the products quantise their rows themselves, and up to 16 */
-/* rows the combine is part of the down product: two or three launches       */
-/* instead of five).                                                         */
+/* (up to 4 tokens, 16 with small experts, the products quantise their rows  */
+/* themselves, and up to 16 rows the combine is then part of the down        */
+/* product: two or three launches instead of five).                          */
 /*   x          bf16 [T][H]; topk_w, group_offsets, sorted_token,            */
 /*              row_of_slot as written by moe_route_permute                  */
 /*   w13_packed, w13_scales  G groups of [2I][H] (gate rows, then up rows)   */

@@ -264,6 +264,46 @@ def test_linear_is_quantise_then_product(M, N, K):
         assert torch.isnan(got[2]).all() and not torch.isnan(got[[0, 1, 3]]).any() and (got[1] == 0).all()
 
 
+@pytest.mark.parametrize("N,K", [(208, 16), (80, 512), (1024, 528), (80, 1024), (272, 1040), (80, 2048), (80, 2064),
+                                 (80, 4096), (9216, 512), (9216, 1024), (9216, 2048)])
+def test_linear_of_few_rows(N, K):
+    """Every row count of the one-launch products (a row is quantised by one to eight waves) and those past them."""
+    rng = np.random.default_rng(N + K)
+    x = _rows(rng, 17, K, 30.0)
+    x[3] = 0
+    w = rng.integers(-128, 128, (N, K), dtype=np.int8)
+    wp, sw = _pack(w[None]), torch.from_numpy(rng.uniform(0.001, 0.02, N).astype(np.float32)).cuda()
+    codes, scales = _quantise(x)
+    want = torch.empty((17, N), dtype=torch.bfloat16, device="cuda")
+    moe.moe_w8a8_gemm(17, N, K, codes, scales, wp, sw, want)
+    xd = to_dev_bf16(x)
+    for M in range(1, 18):
+        got = torch.full((M + 1, N), 3.0, dtype=torch.bfloat16, device="cuda")
+        moe.moe_w8a8_linear(M, N, K, xd, wp, sw, torch.empty_like(codes), torch.empty_like(scales), got)
+        torch.cuda.synchronize()
+        assert torch.equal(got[:M].view(torch.int16), want[:M].view(torch.int16)) and (got[M] == 3.0).all(), M
+
+
+@pytest.mark.parametrize("T", [5, 6, 7, 9, 12, 13, 16, 17])
+@pytest.mark.parametrize("H,I,E,k,ns", [(1024, 512, 16, 4, 1), (512, 128, 16, 1, 0), (4096, 128, 12, 2, 1), (512, 1024, 1, 1, 1)])
+def test_experts_of_few_tokens(T, H, I, E, k, ns):
+    """moe_w8a8_experts of small experts gives the bits of its parts at the token counts around its one-launch products."""
+    case, layer, _ = _experts_case(T, H, I, E, k, ns, T + H)
+    buf = moe.Buffers(case.desc, T, int8=True)
+    layer.forward(case.xd, buf)
+    d, w, R = case.desc, layer.experts, case.desc.rows(T)
+    o = moe.Buffers(d, T, int8=True)
+    moe.moe_act_quant_int8(T, H, case.xd, o.xq8, o.xqs8)
+    moe.moe_w8a8_grouped_gemm(d, T, o.xq8, o.xqs8, buf.sorted_token, T, 2 * I, H, w.w13, w.s13, buf.group_offsets,
+                              moe.MOE_ACT_SWIGLU, o.h)
+    moe.moe_act_quant_int8(R, I, o.h, o.hq8, o.hqs8)
+    moe.moe_w8a8_grouped_gemm(d, T, o.hq8, o.hqs8, None, 0, H, I, w.w2, w.s2, buf.group_offsets, moe.MOE_ACT_NONE, o.y)
+    moe.moe_combine(d, T, o.y, buf.row_of_slot, buf.topk_w, o.out)
+    torch.cuda.synchronize()
+    for name in ("h", "y", "out"):
+        assert torch.equal(getattr(o, name).view(torch.int16), getattr(buf, name).view(torch.int16)), name
+
+
 def _groups(rng, G, R, empty):
     cut = np.sort(rng.integers(0, R + 1, G - 1))
     off = np.concatenate([[0], cut, [R]]).astype(np.int32)

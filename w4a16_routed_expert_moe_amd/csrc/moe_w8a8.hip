@@ -121,17 +121,19 @@ constexpr int kFusedMaxK = 4096;  // 8 elements per thread of 8 waves
 
 // `rows` bf16 rows (row r from source row src_of(r) of x, zeros if that is
 // negative) to INT8 codes in LDS, row r at sq + r (K + 16) -- 16 bytes of
-// padding: 16 rows at one k sit on distinct banks -- and their scales.  Eight
-// waves take a row, eight elements per thread, so W waves take W / 8 rows at
-// a time and kQuantRows times as many between two barriers.  Ends with a
-// barrier.
+// padding: 16 rows at one k sit on distinct banks -- and their scales.  A row
+// takes as many waves as it needs (1, 2, 4 or 8; eight elements per thread),
+// the W waves W divided by that many rows at a time and kQuantRows times as
+// many between two barriers.  Ends with a barrier.
 constexpr int kQuantRows = 4;
+__host__ __device__ inline int log2_waves_per_row(int K) { return K <= 512 ? 0 : K <= 1024 ? 1 : K <= 2048 ? 2 : 3; }
 template <int W, typename F>
 __device__ __forceinline__ void quantise_rows(const uint16_t *__restrict__ x, int K, int rows, F src_of, int8_t *sq,
                                               float *sscale, uint32_t (&smax)[kQuantRows * W]) {
-    constexpr int RB = kQuantRows, GR = W / 8;
-    const int tid = threadIdx.x & 511, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
-    const int gr = wave >> 3, LD = K + 16;
+    constexpr int RB = kQuantRows;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id(), LD = K + 16;
+    const int lw = log2_waves_per_row(K), GR = W >> lw, gr = wave >> lw, part = wave & ((1 << lw) - 1);
+    const int tid = 64 * part + l;  // of the threads of the row
     const bool in = 8 * tid < K;
     for (int r0 = gr; r0 - gr < rows; r0 += RB * GR) {
         u32x4 v[RB];
@@ -156,7 +158,7 @@ __device__ __forceinline__ void quantise_rows(const uint16_t *__restrict__ x, in
             if (r < rows) {
                 uint32_t mx = 0u;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) mx = max(mx, smax[i * W + 8 * gr + w]);
+                for (int w = 0; w < 8; ++w) mx = max(mx, smax[i * W + (gr << lw) + (w & ((1 << lw) - 1))]);
                 const RowScale s = row_scale(mx);
                 if (tid == 0) sscale[r] = s.scale;
                 if (in) *(uint2 *)(sq + (size_t)r * LD + 8 * tid) = quant8(v[i], s);
@@ -420,11 +422,30 @@ void launch_stream(const Args &a, int rows, hipStream_t st) {
         launch_stream_u<ACT, NS, 8, Q>(a, rows, st);
 }
 
-// Rows that a workgroup quantises for itself instead of a launch before (a
-// 4096 x 4096 projection: 5.9 against 8.5 us at 1 row, 6.8 against 8.5 at 4,
-// 9.3 against 8.8 at 8; the layer's experts at hidden 4096: 46 against 49 us
-// at 1 token, 128 against 131 at 4, 226 against 207 at 8).
-constexpr int kFusedRows = 4;
+// Where a product's workgroups quantise its few rows for themselves instead of
+// a launch before.  Dense: up to 4 rows, and as many as quantise_rows takes in
+// one pass, half of that past 8192 columns, where a CU has several workgroups
+// (captured / called one by one, us, against two launches: 4096 x 1024 at 8
+// rows 4.2 / 6.1 against 5.3 / 8.5, at 16 5.2 / 6.1 against 5.5 / 8.6; 4096 x
+// 2048 at 8 5.4 / 6.1 against 6.1 / 8.4, at 12 6.8 / 6.7 against 6.2 / 8.5;
+// 16384 x 2048 at 8 9.6 / 9.3 against 8.4 / 8.4; 4096 x 4096 at 4 6.1 / 6.1
+// against 8.1 / 8.3, at 8 8.5 / 8.5 against 8.1 / 8.3).
+bool fuse_dense(int M, int N, int K) {
+    if (K > kFusedMaxK) return false;
+    return M <= 4 || (M <= 16 && M << log2_waves_per_row(K) <= (N <= 8192 ? 32 : 16));
+}
+// Experts: up to 4 tokens, and up to 16 (12 with longer rows) where the weights
+// are few: then the five launches' latency counts, else the tiled products
+// stream the weights faster (hidden 1024, inter 512, 17 groups, 27 MB: 15.7
+// against 17.1 us captured, 16.1 against 20.6 called one by one at 8 tokens,
+// 17.9 / 18.2 against 17.5 / 20.5 at 16; hidden 4096, inter 128, 12 groups:
+// 13.7 against 21.1 at 12; hidden 2048, inter 256, 9 groups: 13.6 against 18.4
+// at 5, 18.7 against 18.6 at 12, 21.0 against 18.8 at 16; hidden 2048, inter
+// 512, 25 groups, 79 MB: 26.9 against 25.1 at 12; the layer at hidden 4096: 42
+// against 49 at 1 token, 126 against 131 at 4, 149 against 125 at 5).
+bool fuse_experts(int T, int G, int H, int I) {  // H and I are at most 4096 = kFusedMaxK
+    return T <= 4 || (T <= (H <= 1024 ? 16 : 12) && (size_t)3 * G * H * I <= (size_t)32 << 20);
+}
 // Rows up to which the weight stream is the faster kernel.  Dense, 4096 x
 // 4096: 6.2 against 9.5 us at 16 rows.  Grouped: the tiled kernel needs no
 // more bytes and has more of them in flight (the layer's experts: 207 against
@@ -542,7 +563,7 @@ extern "C" moe_status moe_w8a8_linear(int32_t M, int32_t N, int32_t K, const uin
         return MOE_ERR_ALIGN;
     hipStream_t st = (hipStream_t)stream;
     w8::Args p = w8::make_args(1, M, N, K, w_packed, w_scales, out);
-    if (M <= w8::kFusedRows && K <= w8::kFusedMaxK) {
+    if (w8::fuse_dense(M, N, K)) {
         p.x = x;
     } else {
         w8::launch_quant(M, K, x, codes, scales, st);
@@ -606,7 +627,7 @@ extern "C" moe_status moe_w8a8_experts(const moe_layer_desc *desc, int32_t T, co
     const int H = desc->hidden, I = desc->inter, G = desc->n_routed + desc->n_shared;
     const int R = T * (desc->top_k + desc->n_shared);
     hipStream_t st = (hipStream_t)stream;
-    const bool fused = T <= w8::kFusedRows;  // H and I are at most 4096 = kFusedMaxK
+    const bool fused = w8::fuse_experts(T, G, H, I);
     w8::Args p = w8::make_args(G, R, 2 * I, H, w13_packed, w13_scales, h);
     p.gather = sorted_token;
     p.n_src = T;
