@@ -1,4 +1,5 @@
-"""Build ``libmoe_w4a16.so`` (HIP, gfx950) in-tree with hipcc.
+"""Build ``libmoe_w4a16.so`` (HIP, gfx950) in-tree with hipcc, and ``_bind.so``,
+the binding's native argument checks, with g++.
 
 Every HIP source is compiled for gfx950 only, with packed-fp32 code
 generation disabled, and linked into one shared library next to this file.
@@ -9,12 +10,14 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmoe_w4a16.so")
+BIND_PATH = os.path.join(HERE, "_bind.so")
 SOURCES = ["moe_route.hip", "moe_permute.hip", "moe_gemm.hip", "moe_gemm_tiled.hip", "moe_down_combine.hip",
            "moe_decode.hip",
            "moe_combine.hip", "moe_layout.hip", "moe_mx_gemm.hip", "moe_gemm_fp4wide.hip",
@@ -50,10 +53,26 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_bind() -> None:
+    import torch
+    from torch.utils.cpp_extension import TORCH_LIB_PATH, include_paths
+    tmp = BIND_PATH + ".tmp%d" % os.getpid()
+    inc = [a for p in include_paths() + [sysconfig.get_paths()["include"]] for a in ("-isystem", p)]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + inc + [
+           os.path.join(CSRC, "moe_bind.cpp"), "-o", tmp, "-L", TORCH_LIB_PATH, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for moe_bind.cpp:\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(tmp, BIND_PATH)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        bind = ex.submit(_build_bind)
         objs = list(ex.map(_compile, SOURCES))
+        bind.result()
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -61,7 +80,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB_PATH)
     if verbose:
-        print("built", LIB_PATH)
+        print("built", LIB_PATH, BIND_PATH)
     return LIB_PATH
 
 
