@@ -99,6 +99,22 @@ __device__ __forceinline__ int seq_of(const Seqs &q, int t) {
     return __builtin_amdgcn_readfirstlane(min(lo, q.n));
 }
 
+// seq_of with that sequence's bounds (the last one's where there is none):
+// up to 64 sequences take one memory round trip together.
+__device__ __forceinline__ int seq_at(const Seqs &q, int t, int &begin, int &end) {
+    if (q.offsets && q.n <= kWave) {
+        const int i = min(lane_id(), q.n - 1), b = q.offsets[i], e = q.offsets[i + 1];
+        const int s = __popcll(__ballot(lane_id() < q.n && e <= t)), at = min(s, q.n - 1);
+        begin = min(max(__builtin_amdgcn_readlane(b, at), 0), q.T);
+        end = min(max(__builtin_amdgcn_readlane(e, at), 0), q.T);
+        return s;
+    }
+    const int s = seq_of(q, t), at = min(s, q.n - 1);
+    begin = seq_begin(q, at);
+    end = seq_end(q, at);
+    return s;
+}
+
 struct Out {
     int32_t *counts;
     float *prob, *coef, *loss;
@@ -248,11 +264,13 @@ __global__ __launch_bounds__(64 * W) void k_balance_part(Seqs q, const float *__
     tok.load(q, logits, idx, E, k, t0, t1);
     __syncthreads();
     int buf = 0;
-    for (int s = seq_of(q, t0); s < q.n; ++s) {
-        const int begin = seq_begin(q, s), a = max(begin, t0), b = min(seq_end(q, s), t1);
-        if (begin >= t1) break;
+    int begin, end;
+    for (int s = seq_at(q, t0, begin, end); s < q.n && begin < t1;) {
+        const int a = max(begin, t0), b = min(end, t1);
         if (a >= b) {  // empty, and any number after it: on to the one that holds token a
-            s = max(s, seq_of(q, a) - 1);
+            const int to = seq_at(q, a, begin, end);
+            if (to <= s) break;  // (bounds that decrease)
+            s = to;
             continue;
         }
         float prob;
@@ -265,7 +283,9 @@ __global__ __launch_bounds__(64 * W) void k_balance_part(Seqs q, const float *__
             p.cnt[row * E + tid] = cnt;
         }
         if (tid == 0) p.live[row] = live;
-        if (b == t1) break;  // the chunk ends in this sequence
+        if (b == t1 || ++s >= q.n) break;  // the chunk ends in this sequence
+        begin = seq_begin(q, s);
+        end = seq_end(q, s);
     }
 }
 
@@ -494,8 +514,7 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
     // average: c[e] - sum_j c[j] p[j] is the same for c less any constant, and
     // with nearly even counts little is left to cancel.
     auto enter = [&]() {
-        begin = s < q.n ? seq_begin(q, s) : q.T;
-        end = s < q.n ? seq_end(q, s) : q.T;
+        if (s >= q.n) begin = end = q.T;
         if (!d_loss || s >= q.n) return;
         float n[kSlots], sum = 0.0f;
 #pragma unroll
@@ -529,7 +548,7 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
         }
         if (s < 0) {
             dl = d_loss ? *d_loss : 0.0f;
-            s = seq_of(q, t0);
+            s = seq_at(q, t0, begin, end);
             enter();
         }
         if ((unsigned)ek >= (unsigned)E) ek = -1;
@@ -548,13 +567,9 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
         for (int u = 0; u < U; ++u) {
             const int t = tb + u;
             if (t >= t1) break;
-            if (s < q.n && t >= end) {
-                ++s;
+            if (s < q.n && t >= end) {  // the sequence that holds t, past any number of empty ones
+                s = seq_at(q, t, begin, end);
                 enter();
-                if (s < q.n && t >= end) {  // empty, and any number after it
-                    s = max(s + 1, seq_of(q, t));
-                    enter();
-                }
             }
             const bool live = on[u] && s < q.n && t >= begin;
             float slope[kSlots], sum = 0.0f, cs = 0.0f, ds[kSlots] = {0.f, 0.f, 0.f, 0.f};
