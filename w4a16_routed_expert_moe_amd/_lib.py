@@ -72,11 +72,9 @@ def lib() -> ctypes.CDLL:
     """Load the HIP library (raises if it has not been built)."""
     global _lib, _at
     if _lib is None:
-        for path in (LIB_PATH, os.path.join(_HERE, "_bind.so")):
-            if not os.path.exists(path):
-                raise RuntimeError("%s is not built (run __graft_entry__.build() or "
-                                   "python w4a16_routed_expert_moe_amd/build.py); there is no fallback"
-                                   % os.path.basename(path))
+        if not os.path.exists(LIB_PATH):
+            raise RuntimeError("libmoe_w4a16.so is not built (run __graft_entry__.build() or "
+                               "python w4a16_routed_expert_moe_amd/build.py); there is no fallback")
         L = ctypes.CDLL(LIB_PATH)
         P, i32, u64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64, ctypes.c_size_t
         D = ctypes.POINTER(MoeLayerDesc)
@@ -130,9 +128,10 @@ def lib() -> ctypes.CDLL:
         if L.moe_abi_version() != ABI_VERSION:
             raise RuntimeError("libmoe_w4a16.so has ABI version %d, this binding expects %d (rebuild)"
                                % (L.moe_abi_version(), ABI_VERSION))
-        from . import _bind
-        _bind.set_checked(_checked)
-        _at = _bind.at
+        if os.path.exists(os.path.join(_HERE, "_bind.so")):  # else the same checks in Python
+            from . import _bind
+            _bind.set_checked(_checked)
+            _at = _bind.at
         _lib = L
     return _lib
 
