@@ -7,7 +7,7 @@
 //   coef[q] = alpha E / (k n_q^2 Q')
 //
 // The loss reads every logit once and the gradient reads and writes every
-// one once: at 65536 x 256, 67 MB in 23 to 28 us plus 6 us for the sums of the
+// one once: at 65536 x 256, 67 MB in 18 to 22 us plus 6 us for the sums of the
 // chunks, and 134 MB in 27 to 29 us (4.9 TB/s, a copy's rate).  Up to 8192
 // tokens both are bound by latency: 4 to 7 us a launch.  A wave takes a token;
 // a lane holds four experts, so the sum over a token's experts is one wave
@@ -54,17 +54,19 @@ template <bool VEC>
 __device__ __forceinline__ int expert_of(int i) {
     return VEC ? 4 * lane_id() + i : lane_id() + kWave * i;
 }
+// A row's logits; past its end the lane takes others of the row, which no
+// caller uses: a load under a condition would be waited for before the next.
 template <bool VEC>
 __device__ __forceinline__ void load_row(const float *__restrict__ row, int E, float (&x)[kSlots]) {
     if (VEC) {
-        const float4 v = 4 * lane_id() < E ? *(const float4 *)(row + 4 * lane_id()) : float4{0.f, 0.f, 0.f, 0.f};
+        const float4 v = *(const float4 *)(row + min(4 * lane_id(), E - 4));
         x[0] = v.x;
         x[1] = v.y;
         x[2] = v.z;
         x[3] = v.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) x[i] = expert_of<VEC>(i) < E ? row[expert_of<VEC>(i)] : 0.0f;
+        for (int i = 0; i < kSlots; ++i) x[i] = row[min(expert_of<VEC>(i), E - 1)];
     }
 }
 
@@ -79,7 +81,6 @@ __device__ __forceinline__ int seq_begin(const Seqs &q, int s) {
 __device__ __forceinline__ int seq_end(const Seqs &q, int s) {
     return q.offsets ? min(max(q.offsets[s + 1], 0), q.T) : q.T;
 }
-__device__ __forceinline__ bool token_live(const Seqs &q, int t) { return !q.mask || q.mask[t] != 0; }
 
 // The first sequence that ends past token t (n if none): each round the 64
 // lanes probe 64 equally spaced ends, so 64 sequences take one memory round
@@ -177,23 +178,32 @@ struct Tokens {
         const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         float x[U][kSlots];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + wave + u * W;
-            on[u] = t < t1;
-            if (t < t1) {
-                on[u] = token_live(q, t);
-                load_row<VEC>(logits + (size_t)t * E, E, x[u]);
-            }
-        }
+        for (int u = 0; u < U; ++u) on[u] = t0 + wave + u * W < t1;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int at = tid + 64 * W * i;
-            te[i] = t0 + at / k;
+            te[i] = t0 + (tid + 64 * W * i) / k;
             e[i] = -1;
-            if (te[i] < t1) {
-                e[i] = idx[(size_t)t0 * k + at];
-                if (!token_live(q, te[i]) || (unsigned)e[i] >= (unsigned)E) e[i] = -1;
+        }
+        if (t0 < t1) {  // there is a token: every load is of one, and all are in flight together
+#pragma unroll
+            for (int u = 0; u < U; ++u) load_row<VEC>(logits + (size_t)min(t0 + wave + u * W, t1 - 1) * E, E, x[u]);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                e[i] = idx[(size_t)t0 * k + min(tid + 64 * W * i, (t1 - t0) * k - 1)];
+            if (q.mask) {
+                uint8_t m[U], me[NI];
+#pragma unroll
+                for (int u = 0; u < U; ++u) m[u] = q.mask[min(t0 + wave + u * W, t1 - 1)];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) me[i] = q.mask[min(te[i], t1 - 1)];
+#pragma unroll
+                for (int u = 0; u < U; ++u) on[u] = on[u] & (m[u] != 0);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) e[i] = me[i] != 0 ? e[i] : -1;
             }
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (te[i] >= t1 || (unsigned)e[i] >= (unsigned)E) e[i] = -1;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -536,15 +546,18 @@ __global__ __launch_bounds__(256) void k_route_backward(Seqs q, const float *__r
         bool on[U];
         int ek = -1;
         float dw = 0.0f, xk = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            on[u] = true;
+            load_row<VEC>(logits + (size_t)min(tb + u, t1 - 1) * E, E, x[u]);
+        }
         if (d_w && lu < U && lj < k && tb + lu < t1) {
             ek = idx[(size_t)(tb + lu) * k + lj];
             dw = d_w[(size_t)(tb + lu) * k + lj];
         }
+        if (q.mask) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = min(tb + u, t1 - 1);
-            on[u] = token_live(q, t);
-            load_row<VEC>(logits + (size_t)t * E, E, x[u]);
+            for (int u = 0; u < U; ++u) on[u] = q.mask[min(tb + u, t1 - 1)] != 0;
         }
         if (s < 0) {
             dl = d_loss ? *d_loss : 0.0f;
