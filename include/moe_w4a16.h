@@ -595,8 +595,9 @@ moe_status moe_w8a8_experts(const moe_layer_desc *desc, int32_t T, const uint16_
 /*                [n_seq]; loss fp32 [1] (all written)                       */
 /*   ws, ws_bytes workspace of moe_balance_workspace_bytes(desc, T, n_seq)   */
 /*                bytes, 16-byte aligned, zero before the first call (every  */
-/*                call leaves its counter zero); calls that may overlap in   */
-/*                time need distinct workspaces                              */
+/*                call leaves its counter zero); one of that size serves     */
+/*                every smaller T with as many sequences or fewer too; calls */
+/*                that may overlap in time need distinct workspaces          */
 /* Outputs, here and below, overlap neither each other nor an input.         */
 /* Of desc only n_routed and top_k matter here (and routed_scale below).     */
 size_t moe_balance_workspace_bytes(const moe_layer_desc *desc, int32_t T, int32_t n_seq);

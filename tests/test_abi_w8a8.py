@@ -139,3 +139,37 @@ BACKWARD = (64, 2, A, A, A, A, A, A, A, A, A, None)
 ] + [({"_%d" % i: ODD}, ALIGN) for i in (3, 5, 6, 7, 8, 9, 10, 11)])
 def test_route_backward(at, status):
     assert _call("moe_route_backward", (_desc(),) + BACKWARD, **at) == status
+
+
+def _partial_sums_bytes(T, n_seq, E, chunk):
+    """The header, a double per sequence and 64 experts, and per chunk and sequence E sums, E counts and a token count."""
+    rows = -(-T // chunk) + n_seq
+    return 64 + 8 * n_seq * -(-E // 64) + rows * (8 * E + 4) + 4 * n_seq
+
+
+def test_balance_workspace_serves_smaller_calls():
+    """It never shrinks with more tokens or sequences (the tokens of a chunk, and with them the number of chunks, jump at
+    powers of two), and it holds the partial sums of the smallest chunks that a call of that size takes."""
+    f = moe.moe_balance_workspace_bytes
+    edges = sorted({max(0, (1 << i) + j) for i in range(21) for j in (-129, -1, 0, 1, 2, 129)} | {3000, 12289, 50000})
+    edges = [t for t in edges if t <= 1 << 20]
+    for E in (1, 41, 256):
+        d = moe.MoeLayerDesc.make(4096, 2048, E, 1, 0)
+        for S in (1, 7, 65, 3000):
+            sizes = [f(d, t, S) for t in edges]
+            assert all(a <= b for a, b in zip(sizes, sizes[1:])), (E, S)
+            assert all(f(d, t, S) <= f(d, t, S + 1) for t in edges), (E, S)
+        for T, chunk in ((2048, 8), (4096, 16), (8192, 32), (16384, 64), (32768, 64), (65536, 128), (1 << 20, 128)):
+            for S in (1, 65):
+                assert f(d, T, S) >= _partial_sums_bytes(T, S, E, chunk), (E, T, S)
+
+
+def test_balance_workspace_of_another_call_is_accepted():
+    """A call refuses a workspace only where its own partial sums do not fit.  (That of T + 1 tokens was smaller than
+    that of T past 2048, 4096 and 8192 tokens.)"""
+    d = moe.MoeLayerDesc.make(4096, 2048, 256, 6, 1)
+    for T in (2048, 4096, 8192, 32768):
+        least = _partial_sums_bytes(T, 2, 256, 8 * max(1, T // 2048) if T <= 16384 else 64)
+        args = (ctypes.byref(d), T) + LOSS[1:]
+        assert _call("moe_balance_loss", args, _13=least - 1) == WORKSPACE
+        assert moe.moe_balance_workspace_bytes(d, T + 1, 2) >= least

@@ -426,3 +426,22 @@ def test_binding_refusals():
         moe.moe_balance_loss(desc, 64, 2, i, i, f, i, 0.01, i, f, f, f, ws)
     with pytest.raises(ValueError):    # counts are needed with d_loss
         moe.moe_route_backward(desc, 64, 2, i, None, f, i, None, f, f, None, f)
+
+
+def test_one_workspace_for_every_smaller_call():
+    """A workspace sized for 8193 tokens and 9 sequences, allocated once, in turn through calls of other sizes, those with
+    more partial sums among them."""
+    say("balance, one workspace")
+    rng = np.random.default_rng(13)
+    E, k = 64, 3
+    ws = None
+    for T, S in ((8193, 9), (8192, 9), (2048, 2), (8193, 1), (100, 3), (4096, 8), (0, 9), (8000, 9)):
+        x, idx = _inputs(rng, T, E, k)
+        off = _cuts(rng, T, S)
+        d_w = rng.standard_normal((T, k)).astype(np.float32)
+        st = Step(x, idx, off, None, k, d_w=d_w)
+        if ws is None:
+            ws = st.ws
+        st.ws = ws
+        st.run()
+        _check(st, _reference(x, idx, off, None, k, 0.01, 1.0, 1.0, d_w), T)

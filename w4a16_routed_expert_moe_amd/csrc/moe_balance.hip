@@ -12,6 +12,8 @@
 // tokens both are bound by latency: 4 to 7 us a launch.  A wave takes a token;
 // a lane holds four experts, so the sum over a token's experts is one wave
 // reduction and the sums over tokens stay in registers.
+#include <algorithm>
+
 #include "moe_route_common.h"
 
 namespace moe {
@@ -35,6 +37,14 @@ int chunk_tokens(int T) {
     return C;
 }
 int chunk_count(int T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
+// The most chunks of any call with up to T tokens, which is not always that of
+// T: where the chunk's length doubles (past 2048, 4096, ..., 32768 tokens) the
+// count halves.
+int most_chunks(int T) {
+    int n = chunk_count(T);
+    for (int64_t t = (int64_t)kMinChunk * kChunks; t < T; t *= 2) n = std::max(n, chunk_count((int)t));
+    return n;
+}
 
 // Sigmoid s and its slope s (1 - s) from e = exp(-|x|), which neither
 // overflows nor cancels: s = 1 / (1 + e) or e / (1 + e), slope = e / (1 + e)^2.
@@ -651,7 +661,7 @@ using namespace moe;
 
 extern "C" size_t moe_balance_workspace_bytes(const moe_layer_desc *desc, int32_t T, int32_t n_seq) {
     if (check_desc(desc) != MOE_OK || check_tokens(T) != MOE_OK || n_seq < 1 || n_seq > MOE_MAX_TOKENS) return 0;
-    return (parts_bytes(chunk_count(T), n_seq, desc->n_routed) + 255) / 256 * 256;
+    return (parts_bytes(most_chunks(T), n_seq, desc->n_routed) + 255) / 256 * 256;
 }
 
 extern "C" moe_status moe_balance_loss(const moe_layer_desc *desc, int32_t T, int32_t n_seq,
@@ -665,8 +675,8 @@ extern "C" moe_status moe_balance_loss(const moe_layer_desc *desc, int32_t T, in
     if (!aligned(ws, 16) || !aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(counts, 4) ||
         !aligned(prob_sums, 4) || !aligned(seq_coef, 4) || !aligned(loss, 4))
         return MOE_ERR_ALIGN;
-    if (ws_bytes < moe_balance_workspace_bytes(desc, T, n_seq)) return MOE_ERR_WORKSPACE;
     const int E = desc->n_routed, k = desc->top_k;
+    if (ws_bytes < parts_bytes(chunk_count(T), n_seq, E)) return MOE_ERR_WORKSPACE;  // what this call uses
     hipStream_t st = (hipStream_t)stream;
     const Seqs q{seq_offsets, token_mask, n_seq, T};
     const Out o{counts, prob_sums, seq_coef, loss};
