@@ -1,4 +1,6 @@
 """The native argument check of the binding against the Python one (CPU tensors: device -1)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -64,3 +66,15 @@ def test_a_tensor_without_memory_is_an_error(at):
         torch.func.vmap(lambda row: row + at(-1, row, "row", torch.float32, 8))(t)
     with pytest.raises((RuntimeError, ValueError)):
         at(0, torch.zeros(8, device="meta"), "x", torch.float32, 8)
+
+
+def test_a_copy_on_write_tensor_gets_memory_of_its_own(at):
+    """The address may be written through: it is not the one that the other tensor still reads."""
+    for whose in ("clone", "origin"):
+        origin = torch.arange(8, dtype=torch.float32)
+        clone = torch._lazy_clone(origin)
+        written, other = (clone, origin) if whose == "clone" else (origin, clone)
+        p = at(-1, written, "out", torch.float32, 8)
+        ctypes.memset(p, 0, 32)
+        assert p == written.data_ptr() != other.data_ptr()
+        assert torch.equal(other, torch.arange(8, dtype=torch.float32)) and not written.any(), whose

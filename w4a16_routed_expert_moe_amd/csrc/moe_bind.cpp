@@ -31,7 +31,9 @@ PyObject *at(PyObject *, PyObject *const *args, Py_ssize_t n) {
         try {
             if (t.layout() == c10::kStrided && t.get_device() == dev &&
                 t.scalar_type() == ((THPDtype *)args[3])->scalar_type && t.is_contiguous() && t.numel() >= numel)
-                return PyLong_FromVoidPtr(const_cast<void *>(t.const_data_ptr()));
+                // the address to write through, as Tensor.data_ptr() gives it:
+                // a copy-on-write tensor gets memory of its own first
+                return PyLong_FromVoidPtr(t.mutable_data_ptr());
         } catch (const std::exception &) {  // a tensor without memory (one that torch.func wraps, say)
         }
     }
