@@ -1,5 +1,7 @@
 """Build ``libmoe_w4a16.so`` (HIP, gfx950) in-tree with hipcc, and ``_bind.so``,
-the binding's native argument checks, with g++.
+the binding's native argument checks, with g++.  The library needs hipcc only:
+where g++ or the headers of Python or torch are missing, the binding's checks
+stay in Python.
 
 Every HIP source is compiled for gfx950 only, with packed-fp32 code
 generation disabled, and linked into one shared library next to this file.
@@ -8,9 +10,11 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shlex
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -53,12 +57,12 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_bind() -> None:
+def _compile_bind() -> None:
     import torch
     from torch.utils.cpp_extension import TORCH_LIB_PATH, include_paths
     tmp = BIND_PATH + ".tmp%d" % os.getpid()
     inc = [a for p in include_paths() + [sysconfig.get_paths()["include"]] for a in ("-isystem", p)]
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    cmd = shlex.split(os.environ.get("CXX", "g++")) + ["-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + inc + [
            os.path.join(CSRC, "moe_bind.cpp"), "-o", tmp, "-L", TORCH_LIB_PATH, "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -67,12 +71,24 @@ def _build_bind() -> None:
     os.replace(tmp, BIND_PATH)
 
 
+def _build_bind() -> bool:
+    """Whether the native checks could be built; if not, none of an earlier build are left in their place."""
+    try:
+        _compile_bind()
+        return True
+    except (RuntimeError, OSError, ImportError) as e:
+        if os.path.exists(BIND_PATH):
+            os.remove(BIND_PATH)
+        warnings.warn("_bind.so is not built, arguments are checked in Python: %s" % e)
+        return False
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         bind = ex.submit(_build_bind)
         objs = list(ex.map(_compile, SOURCES))
-        bind.result()
+        native = bind.result()
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -80,7 +96,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB_PATH)
     if verbose:
-        print("built", LIB_PATH, BIND_PATH)
+        print("built", LIB_PATH, BIND_PATH if native else "")
     return LIB_PATH
 
 
