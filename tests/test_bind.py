@@ -1,5 +1,8 @@
 """The native argument check of the binding against the Python one (CPU tensors: device -1)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -78,3 +81,34 @@ def test_a_copy_on_write_tensor_gets_memory_of_its_own(at):
         ctypes.memset(p, 0, 32)
         assert p == written.data_ptr() != other.data_ptr()
         assert torch.equal(other, torch.arange(8, dtype=torch.float32)) and not written.any(), whose
+
+
+@pytest.mark.parametrize("how", ["of another torch", "without a version", "not loadable"])
+def test_native_checks_of_another_build_are_not_used(how):
+    """A _bind.so that was built for another torch reads tensors at the wrong offsets: the Python checks take its place."""
+    program = """
+import sys, types, warnings
+import torch
+import w4a16_routed_expert_moe_amd as moe
+name = "w4a16_routed_expert_moe_amd._bind"
+other = types.ModuleType(name)
+other.at = other.set_checked = lambda *a: sys.exit("the other build's check was used")
+other.built_for = "Python 3.10, torch 1.0"
+how = sys.argv[1]
+if how == "without a version":
+    del other.built_for
+sys.modules[name] = None if how == "not loadable" else other
+moe._bind = other
+if how == "not loadable":
+    del moe._bind
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    moe._lib.lib()
+assert moe._lib._at is moe._lib._checked
+assert any("rebuild" in str(w.message) for w in seen), seen
+t = torch.zeros(8)
+assert moe._lib._at(-1, t, "t", torch.float32, 8) == t.data_ptr()
+"""
+    r = subprocess.run([sys.executable, "-c", program, how], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr

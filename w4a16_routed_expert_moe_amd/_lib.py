@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -128,12 +129,28 @@ def lib() -> ctypes.CDLL:
         if L.moe_abi_version() != ABI_VERSION:
             raise RuntimeError("libmoe_w4a16.so has ABI version %d, this binding expects %d (rebuild)"
                                % (L.moe_abi_version(), ABI_VERSION))
-        if os.path.exists(os.path.join(_HERE, "_bind.so")):  # else the same checks in Python
-            from . import _bind
-            _bind.set_checked(_checked)
-            _at = _bind.at
+        _at = _native_at() or _checked
         _lib = L
     return _lib
+
+
+def _native_at():
+    """The native form of _checked, or None: without _bind.so, or with one built for another Python or torch (it reads
+    their objects at the offsets of the headers it was compiled with), the same checks are made in Python."""
+    if not os.path.exists(os.path.join(_HERE, "_bind.so")):
+        return None
+    from .build import bind_built_for
+    try:
+        from . import _bind
+        built_for = _bind.built_for
+    except (ImportError, AttributeError) as e:
+        built_for = e
+    if built_for != bind_built_for():
+        warnings.warn("_bind.so is not one for %s (%s), arguments are checked in Python (rebuild)"
+                      % (bind_built_for(), built_for))
+        return None
+    _bind.set_checked(_checked)
+    return _bind.at
 
 
 def _check(fn: str, status: int):

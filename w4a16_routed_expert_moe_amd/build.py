@@ -57,12 +57,19 @@ def _compile(src: str) -> str:
     return obj
 
 
+def bind_built_for() -> str:
+    """What _bind.so has to be built for to be used in this process."""
+    import torch
+    return "Python %d.%d, torch %s" % (sys.version_info[0], sys.version_info[1], torch.__version__)
+
+
 def _compile_bind() -> None:
     import torch
     from torch.utils.cpp_extension import TORCH_LIB_PATH, include_paths
     tmp = BIND_PATH + ".tmp%d" % os.getpid()
     inc = [a for p in include_paths() + [sysconfig.get_paths()["include"]] for a in ("-isystem", p)]
     cmd = shlex.split(os.environ.get("CXX", "g++")) + ["-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-DMOE_BUILT_FOR=\"%s\"" % bind_built_for(),
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + inc + [
            os.path.join(CSRC, "moe_bind.cpp"), "-o", tmp, "-L", TORCH_LIB_PATH, "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
