@@ -568,8 +568,8 @@ moe_status moe_w8a8_experts(const moe_layer_desc *desc, int32_t T, const uint16_
 /* ---------------------------------------------------------------------- */
 /* Balance of the router: how many tokens each expert gets, a loss that     */
 /* grows with the imbalance, and the gradient of the router's logits.        */
-/* With the scores of moe_route, s[t][e] = sigmoid(logits[t][e]) (to fp32    */
-/* rounding; below 2^-126 they count as 0), and                              */
+/* With the scores of moe_route, s[t][e] = sigmoid(logits[t][e]) (here within */
+/* 5 units of 2^-23; below 2^-126 they count as 0), and                      */
 /* p[t][e] = s[t][e] / sum_j s[t][j] (0 when every score of the token is 0), */
 /* for the packed sequences q = [seq_offsets[q], seq_offsets[q+1]) with n_q  */
 /* live tokens (those whose token_mask is not 0):                            */

@@ -445,3 +445,43 @@ def test_one_workspace_for_every_smaller_call():
         st.ws = ws
         st.run()
         _check(st, _reference(x, idx, off, None, k, 0.01, 1.0, 1.0, d_w), T)
+
+
+def _token_by_token(x, idx, k, alpha, d_loss, d_w):
+    """_reference where every token is a sequence of its own, with the slope s (1 - s) as e / (1 + e)^2, e = exp(-|x|):
+    1 - s is 0 in fp64 from x = 37 on."""
+    T, E = x.shape
+    counts, prob, coef, loss, _, _, n = _reference(x, idx, np.arange(T + 1), None, k, alpha, 1.0, d_loss, d_w)
+    x = x.astype(np.float64)
+    e = np.exp(-np.abs(x))
+    s, slope = np.where(x < 0, e, 1.0) / (1 + e), e / (1 + e) ** 2
+    ds, size = np.zeros_like(x), np.zeros_like(x)
+    for t in range(T):
+        if d_loss is not None:
+            c = d_loss * coef[t] * counts[t]
+            ds[t] = (c - (c * prob[t]).sum()) / s[t].sum()
+            size[t] = (np.abs(c) + np.abs(c * prob[t]).sum()) / s[t].sum()
+        si = s[t, idx[t]]
+        ds[t, idx[t]] += (d_w[t] - (d_w[t] * si).sum() / si.sum()) / si.sum()
+        size[t, idx[t]] += (np.abs(d_w[t]) + (np.abs(d_w[t]) * si).sum() / si.sum()) / si.sum()
+    return counts, prob, coef, loss, ds * slope, size * slope, n
+
+
+@pytest.mark.parametrize("T", [24, 300])
+@pytest.mark.parametrize("low,high", [(-80.0, -20.0), (-80.0, 80.0), (-30.0, -8.0)])
+def test_far_logits(T, low, high):
+    """The bounds hold whatever the logits' size.  In units of 2^-23 a score is within 5 (exponential 1, its argument 2, the
+    rest of that and the sum with 1 a half each, reciprocal 1), a probability within 17 (score 5, the sum's scores 5 and its
+    ten levels a half each, reciprocal 1, product a half); the gradient's factors as before.  Every sequence is one token,
+    so that no average hides an error; no probability is below 2^-126."""
+    rng = np.random.default_rng(int(T + high))
+    E, k = 256, 6
+    x = rng.uniform(low, high, (T, E)).astype(np.float32)
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    d_w = rng.standard_normal((T, k)).astype(np.float32)
+    st = Step(x, idx, np.arange(T + 1), None, k, d_w=d_w).run()
+    ref = _token_by_token(x, idx, k, 0.01, 1.0, d_w)
+    _check(st, ref, 1)
+    assert (np.abs(st.prob[:-1].double().cpu().numpy() - ref[1]) <= 17 * 2.0 ** -23 * ref[1]).all()
+    one = Step(x[:6], idx[:6], np.arange(7), None, k, d_loss=None, d_w=d_w[:6]).run()  # the one-launch form
+    _check(one, _token_by_token(x[:6], idx[:6], k, 0.01, None, d_w[:6]), 1)
