@@ -83,3 +83,32 @@ def test_the_wait_covers_the_loads_into_lds():
                 assert len(loads) - len(into_lds) == 2 * nsw, (name, loads)
                 seen += 1
     assert seen >= 2 * len(kernels)
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not found")
+def test_every_loop_of_every_kernel_is_looked_at():
+    """An instance of MC m-tiles has MC / 2 k loops (2, 4, ... MC m-tiles that have rows), of pf / 2 steps each: all of them
+    are found, so that the check above leaves none out, and no load into LDS stands in a loop that it does not know."""
+    from w4a16_routed_expert_moe_amd import build as b
+    d = tempfile.mkdtemp(prefix="moe_asm_")
+    try:
+        out = os.path.join(d, "tiled.s")
+        flags = [f for f in b.FLAGS if f != "-fPIC"] + b.EXTRA.get("moe_w8a8_tiled.hip", [])
+        r = subprocess.run([HIPCC] + flags + ["--cuda-device-only", "-S", "-o", out,
+                                              os.path.join(b.CSRC, "moe_w8a8_tiled.hip")], capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+        kernels = _kernels(open(out).read().splitlines())
+    finally:
+        shutil.rmtree(d, ignore_errors=True)
+    for name, body in kernels.items():
+        act, nsw, mc, pf, st, occ = map(int, re.search(r"ILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)E", name).groups())
+        loops = _loops(body)
+        assert len(loops) == mc // 2, (name, len(loops))
+        # matrix instructions of a step: two half steps of C m-tiles times nsw subtiles
+        products = sorted(sum(x.startswith("v_mfma") for x in loop) for loop in loops)
+        assert products == [2 * c * nsw * (pf // 2) for c in range(2, mc + 1, 2)], (name, products)
+        # loads into LDS outside the loops: the prologue's ST - 1 steps and the tail's pf / 2 - 1, of every instance
+        total = sum(x.startswith("global_load_lds") for x in body)
+        inside = sum(x.startswith("global_load_lds") for loop in loops for x in loop)
+        per_step = sum(c // 2 for c in range(2, mc + 1, 2))
+        assert inside == per_step * (pf // 2) and total - inside == per_step * (st - 1 + pf // 2 - 1), (name, total, inside)
