@@ -578,3 +578,23 @@ def test_every_tensor_is_on_the_current_device():
                 call[at] = call[at].as_subclass(Away)
                 with pytest.raises(ValueError, match="device"):
                     fn(*call)
+
+
+@pytest.mark.parametrize("T", [1, 6, 200, 900])
+def test_another_stream_that_waits_for_the_inputs(T):
+    """The layer on a stream of its own, which waits for the stream that filled the inputs, the weights and the workspaces,
+    as a caller has to: the bits of the eager call, also after another batch in the same buffers."""
+    case, layer, _ = _experts_case(T, 1024, 256, 8, 2, 1, 9)
+    eager, buf = moe.Buffers(case.desc, T, int8=True), moe.Buffers(case.desc, T, int8=True)
+    x = case.xd.clone()
+    side = torch.cuda.Stream()
+    for i in range(3):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            layer.forward(x, buf)
+        torch.cuda.current_stream().wait_stream(side)
+        layer.forward(x, eager)
+        torch.cuda.synchronize()
+        for name in ("h", "y", "out"):
+            assert torch.equal(getattr(buf, name).view(torch.int16), getattr(eager, name).view(torch.int16)), (i, name)
+        x.copy_(case.xd.flip(1) * (i + 2.0))
