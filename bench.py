@@ -85,11 +85,17 @@ def dominant_kernel(T, fmt="int4"):
 
 
 def kernel_source_hash(files):
+    """Of the kernel's sources and the flags that they are compiled with (not
+    of the build script, whose other changes leave the kernel as it is)."""
     import hashlib
+    from w4a16_routed_expert_moe_amd import build as b
     h = hashlib.sha256()
-    for f in files + ["../build.py"]:
+    for f in files:
         with open(os.path.join(CSRC, f), "rb") as fh:
             h.update(fh.read())
+        if f.endswith(".hip"):
+            flags = [os.path.relpath(x, b.ROOT) if os.path.isabs(x) else x for x in b.FLAGS + b.EXTRA.get(f, [])]
+            h.update("\0".join(flags).encode())
     return h.hexdigest()[:16]
 
 

@@ -61,3 +61,29 @@ def test_committed_summaries_are_well_formed():
             rec = json.load(open(os.path.join(ROOT, "profiles", f)))
             assert rec["traffic_bytes_per_launch"] > 0
             assert 1.5 < rec["fetch_scale"] < 2.5 and 0.9 < rec["write_scale"] < 1.1
+
+
+def test_a_counter_summary_outlives_changes_that_leave_its_kernel_alone(tmp_path, monkeypatch):
+    """The build script's text, another kernel's source and another file's flags do not change a kernel's hash; its own
+    source and flags do."""
+    import shutil
+    from w4a16_routed_expert_moe_amd import build as b
+    csrc = tmp_path / "csrc"
+    shutil.copytree(bench.CSRC, csrc)
+    shutil.copy(os.path.join(b.HERE, "build.py"), tmp_path)
+    monkeypatch.setattr(bench, "CSRC", str(csrc))
+    _, _, files = bench.dominant_kernel(64)
+    first = bench.kernel_source_hash(files)
+    with open(tmp_path / "build.py", "a") as f:
+        f.write("# another source in the library\n")
+    with open(csrc / "moe_combine.hip", "a") as f:
+        f.write("// changed\n")
+    monkeypatch.setitem(b.EXTRA, "moe_combine.hip", ["-O1"])
+    assert bench.kernel_source_hash(files) == first
+    monkeypatch.setitem(b.EXTRA, "moe_gemm.hip", b.EXTRA["moe_gemm.hip"] + ["-O1"])
+    assert bench.kernel_source_hash(files) != first
+    monkeypatch.setitem(b.EXTRA, "moe_gemm.hip", b.EXTRA["moe_gemm.hip"][:-1])
+    assert bench.kernel_source_hash(files) == first
+    with open(csrc / "moe_gemm_common.h", "a") as f:
+        f.write("// changed\n")
+    assert bench.kernel_source_hash(files) != first
