@@ -468,7 +468,10 @@ moe_status moe_fp8_prepack(int32_t N, int32_t K, const uint8_t *w_canonical, uin
 /*   acc[m][n] = sum_k a[m][k] * w[n][k]      exact, in int32                */
 /*   out[m][n] = bf16( acc * a_scales[m] * w_scales[n] )                     */
 /* The sum is exact whatever its order, so the dense, the grouped and the    */
-/* one-launch forms give the same bits for the same codes and scales.        */
+/* one-launch forms give the same bits for the same codes and scales.  The   */
+/* two products are fp32, from left to right: where acc * a_scales[m] leaves */
+/* fp32's range (rows with values past about 1e31, or none above about       */
+/* 1e-36) the output does too, or loses digits, whatever w_scales[n] is.     */
 /* Outputs and scratch overlap neither each other nor an input.              */
 
 /* Quantisation of each row by itself, symmetric: with amax = max |a[r][k]|  */

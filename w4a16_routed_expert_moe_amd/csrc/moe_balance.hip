@@ -7,9 +7,9 @@
 //   coef[q] = alpha E / (k n_q^2 Q')
 //
 // The loss reads every logit once and the gradient reads and writes every
-// one once: at 65536 x 256, 67 MB in 18 to 22 us plus 6 us for the sums of the
-// chunks, and 134 MB in 27 to 29 us (4.9 TB/s, a copy's rate).  Up to 8192
-// tokens both are bound by latency: 4 to 7 us a launch.  A wave takes a token;
+// one once: at 65536 x 256, 67 MB in 19 to 24 us plus 6 us for the sums of the
+// chunks, and 134 MB in 28 to 29 us (4.7 TB/s, near a copy's rate).  Up to 8192
+// tokens both are bound by latency: 4 to 9 us a launch.  A wave takes a token;
 // a lane holds four experts, so the sum over a token's experts is one wave
 // reduction and the sums over tokens stay in registers.
 #include <algorithm>
@@ -22,13 +22,23 @@ namespace {
 constexpr int kSlots = 4;          // experts per lane: E <= 256
 constexpr int kMaxExperts = kSlots * kWave;
 // Up to here the loss is one workgroup's work, one launch: about 0.8 us per
-// sequence.  Loss + gradient of 33 tokens of 256 experts, us, against two
-// launches for the loss: 1 sequence 8.1 / 10.9, 4 10.4 / 11.6, 8 13.5 / 12.4,
-// 32 32.6 / 15.5; of 128 tokens 11.0 / 11.2, 13.3 / 11.4, 16.6 / 12.6.  Called
-// one by one, the host's 14 to 15 with one launch and 17.5 with two count.
+// sequence.  Loss + gradient of 256 experts, us, captured / called one by one,
+// against two launches for the loss:
+//   8 tokens, 6 sequences     9.0 / 10.3   12.8 / 12.9
+//   33 tokens, 1 sequence     8.2 / 10.4   10.7 / 12.9
+//              4             10.6 / 10.7   11.9 / 12.9
+//              6             12.1 / 12.3   12.1 / 12.9
+//   128 tokens, 1 sequence   10.7 / 11.0   11.2 / 15.0
+//               4            13.1 / 13.4   11.6 / 14.6
+//               6            14.7 / 15.1   11.7 / 14.9
+// The bounds are where the calls one by one, which the host's launches weigh
+// on, break even.
 constexpr int kOneTokens = 128, kOneSeqs = 6;
-constexpr int kChunks = 256;       // token chunks of the partial sums: one per CU ...
-constexpr int kMinChunk = 8, kMaxChunk = 128;  // ... of at least 8 tokens and at most as many as fit the registers
+// Token chunks of the partial sums: one per CU, past 16384 tokens two, of at
+// least 8 tokens and at most as many as fit the registers (past 65536 tokens
+// the chunks stay as long and get more: 8192 at 2^20).
+constexpr int kChunks = 256;
+constexpr int kMinChunk = 8, kMaxChunk = 128;
 
 // the tokens of one chunk, a power of two
 int chunk_tokens(int T) {

@@ -298,9 +298,11 @@ void launch(int act, Args a, hipStream_t st) {
 
 // Which tile: the one with the least cost times rounds of one workgroup per
 // CU.  A larger tile reads fewer bytes per product (what bounds a CU that has
-// its workgroup), a smaller one fills the CUs with fewer rows; a second
-// workgroup on some of the CUs costs nearly a second round.  The costs are
-// the times of one round at N = K = 4096, 8 to 30 us; measured there, us
+// its workgroup), a smaller one fills the CUs with fewer rows; where every CU
+// gets a second workgroup that costs nearly a second round, and a few too many
+// are counted as one too, which was not measured (61 rows of 8208 columns: 258
+// workgroups of 32 x 64 count as two rounds, so 130 of 32 x 128 are taken).
+// The costs are the times of one round at N = K = 4096, 8 to 30 us; us there
 // (tiles of rows x weight rows):
 //   rows       128 x 256   64 x 256   64 x 128   32 x 128   32 x 64
 //   61              18.1       16.7       12.2        9.8       7.7
