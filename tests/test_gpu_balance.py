@@ -485,3 +485,23 @@ def test_far_logits(T, low, high):
     assert (np.abs(st.prob[:-1].double().cpu().numpy() - ref[1]) <= 17 * 2.0 ** -23 * ref[1]).all()
     one = Step(x[:6], idx[:6], np.arange(7), None, k, d_loss=None, d_w=d_w[:6]).run()  # the one-launch form
     _check(one, _token_by_token(x[:6], idx[:6], k, 0.01, None, d_w[:6]), 1)
+
+
+def test_mask_of_truth_values():
+    """A torch.bool mask, which comparisons give, is the uint8 mask of the same bytes; a strided one is refused as any."""
+    rng = np.random.default_rng(17)
+    T, E, k = 200, 24, 2
+    x, idx = _inputs(rng, T, E, k)
+    mask = (rng.random(T) >= 0.3).astype(np.uint8)
+    off = np.array([0, 90, T])
+    d_w = rng.standard_normal((T, k)).astype(np.float32)
+    want = Step(x, idx, off, mask, k, d_w=d_w).run()
+    got = Step(x, idx, off, mask, k, d_w=d_w)
+    got.mask = got.mask != 0
+    assert got.mask.dtype is torch.bool
+    got.run()
+    _check(got, _reference(x, idx, off, mask, k, 0.01, 1.0, 1.0, d_w), T)
+    assert torch.equal(got.d_logits, want.d_logits) and torch.equal(got.prob, want.prob)
+    got.mask = (torch.zeros(2 * T, device="cuda") == 0)[::2]
+    with pytest.raises(ValueError, match="token_mask must be contiguous"):
+        got.run()

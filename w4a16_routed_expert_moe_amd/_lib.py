@@ -556,13 +556,18 @@ def moe_balance_workspace_bytes(desc: MoeLayerDesc, T: int, n_seq: int) -> int:
     return int(lib().moe_balance_workspace_bytes(ctypes.byref(desc), T, n_seq))
 
 
+def _mask(m):
+    """A mask of truth values as the bytes it consists of."""
+    return m.view(_U8) if isinstance(m, _Tensor) and m.dtype is torch.bool else m
+
+
 def moe_balance_loss(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_mask, logits, topk_idx, alpha: float,
                      counts, prob_sums, seq_coef, loss, ws, stream=None):
     E, k = desc.n_routed, desc.top_k
     d = torch.cuda.current_device()
     _check("moe_balance_loss", lib().moe_balance_loss(
         ctypes.byref(desc), T, n_seq, _at(d, seq_offsets, "seq_offsets", _I32, n_seq + 1, True),
-        _at(d, token_mask, "token_mask", _U8, T, True), _at(d, logits, "logits", _F32, T * E),
+        _at(d, _mask(token_mask), "token_mask", _U8, T, True), _at(d, logits, "logits", _F32, T * E),
         _at(d, topk_idx, "topk_idx", _I32, T * k), alpha, _at(d, counts, "counts", _I32, n_seq * E),
         _at(d, prob_sums, "prob_sums", _F32, n_seq * E), _at(d, seq_coef, "seq_coef", _F32, n_seq),
         _at(d, loss, "loss", _F32, 1), _at(d, ws, "ws", _U8, 0), ws.numel(), _stream(stream, d)))
@@ -574,7 +579,7 @@ def moe_route_backward(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, toke
     d = torch.cuda.current_device()
     _check("moe_route_backward", lib().moe_route_backward(
         ctypes.byref(desc), T, n_seq, _at(d, seq_offsets, "seq_offsets", _I32, n_seq + 1, True),
-        _at(d, token_mask, "token_mask", _U8, T, True), _at(d, logits, "logits", _F32, T * E),
+        _at(d, _mask(token_mask), "token_mask", _U8, T, True), _at(d, logits, "logits", _F32, T * E),
         _at(d, topk_idx, "topk_idx", _I32, T * k),
         _at(d, counts, "counts", _I32, n_seq * E, d_loss is None),
         _at(d, seq_coef, "seq_coef", _F32, n_seq, d_loss is None),
