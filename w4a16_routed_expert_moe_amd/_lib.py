@@ -200,6 +200,16 @@ def _checked(dev, t, name, dtype, numel, optional=False):
     return p
 
 
+# What the sizes of a call, or-ed, have above 31 bits when each fits an int32
+# (all non-negative, or one negative, which the library refuses): ctypes would
+# cut a wider one to another size than the tensors are checked for.
+_I32_HIGH = (0, -1)
+
+
+def _wide(fn):
+    raise ValueError("%s: a size does not fit 32 bits" % fn)
+
+
 _at = _checked  # until lib() puts the native one in its place: the common case at 0.05 us a tensor instead of 0.3
 
 
@@ -474,6 +484,8 @@ def moe_fp8_prepack(N: int, K: int, w_canonical, w_packed, stream=None):
 
 # ------------------------------------------------------------------ W8A8
 def moe_act_quant_int8(rows: int, K: int, a, codes, scales, stream=None):
+    if (rows | K) >> 31 not in _I32_HIGH:
+        _wide("moe_act_quant_int8")
     d = torch.cuda.current_device()
     _check("moe_act_quant_int8", lib().moe_act_quant_int8(
         rows, K, _at(d, a, "a", _BF16, rows * K), _at(d, codes, "codes", _I8, rows * K),
@@ -482,6 +494,8 @@ def moe_act_quant_int8(rows: int, K: int, a, codes, scales, stream=None):
 
 def moe_w8a8_packed_bytes(n_groups: int, N: int, K: int) -> int:
     """Bytes of the packed weights of n_groups matrices [N][K] (0 when a size is invalid)."""
+    if (n_groups | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_w8a8_packed_bytes")
     return int(lib().moe_w8a8_packed_bytes(n_groups, N, K))
 
 
@@ -491,6 +505,8 @@ def _packed(n_groups: int, N: int, K: int) -> int:
 
 
 def moe_w8a8_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stream=None):
+    if (n_groups | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_w8a8_prepack")
     d = torch.cuda.current_device()
     _check("moe_w8a8_prepack", lib().moe_w8a8_prepack(
         n_groups, N, K, _at(d, w_canonical, "w_canonical", _I8, n_groups * N * K),
@@ -498,6 +514,8 @@ def moe_w8a8_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, strea
 
 
 def moe_w8a8_gemm(M: int, N: int, K: int, a, a_scales, w_packed, w_scales, out, stream=None):
+    if (M | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_w8a8_gemm")
     d = torch.cuda.current_device()
     _check("moe_w8a8_gemm", lib().moe_w8a8_gemm(
         M, N, K, _at(d, a, "a", _I8, M * K), _at(d, a_scales, "a_scales", _F32, M),
@@ -507,6 +525,8 @@ def moe_w8a8_gemm(M: int, N: int, K: int, a, a_scales, w_packed, w_scales, out, 
 
 def moe_w8a8_linear(M: int, N: int, K: int, x, w_packed, w_scales, codes, scales, out, stream=None):
     """moe_act_quant_int8 + moe_w8a8_gemm in one call; codes and scales are scratch."""
+    if (M | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_w8a8_linear")
     d = torch.cuda.current_device()
     _check("moe_w8a8_linear", lib().moe_w8a8_linear(
         M, N, K, _at(d, x, "x", _BF16, M * K),
@@ -517,6 +537,8 @@ def moe_w8a8_linear(M: int, N: int, K: int, x, w_packed, w_scales, codes, scales
 
 def moe_w8a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_src: int, N: int, K: int,
                           w_packed, w_scales, group_offsets, act: int, out, stream=None):
+    if (T | N | K | act) >> 31 not in _I32_HIGH or n_src >> 31 not in _I32_HIGH:  # (n_src is not used without a_gather)
+        _wide("moe_w8a8_grouped_gemm")
     G, R = desc.groups, desc.rows(T)
     a_rows = n_src if a_gather is not None else R
     out_cols = N // 2 if act == MOE_ACT_SWIGLU else N
@@ -534,6 +556,8 @@ def moe_w8a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_s
 def moe_w8a8_experts(desc: MoeLayerDesc, T: int, x, topk_w, group_offsets, sorted_token, row_of_slot, w13_packed,
                      w13_scales, w2_packed, w2_scales, xq, xqs, h, hq, hqs, y, out, stream=None):
     """Everything after the routing for INT8 experts; xq, xqs, hq and hqs are scratch."""
+    if T >> 31 not in _I32_HIGH:
+        _wide("moe_w8a8_experts")
     H, I, G, R, S = desc.hidden, desc.inter, desc.groups, desc.rows(T), desc.top_k + desc.n_shared
     d = torch.cuda.current_device()
     _check("moe_w8a8_experts", lib().moe_w8a8_experts(
@@ -553,6 +577,8 @@ def moe_w8a8_experts(desc: MoeLayerDesc, T: int, x, topk_w, group_offsets, sorte
 # ------------------------------------------------------------------ router balance and gradient
 def moe_balance_workspace_bytes(desc: MoeLayerDesc, T: int, n_seq: int) -> int:
     """Bytes of the workspace moe_balance_loss needs (0 when a size is invalid)."""
+    if (T | n_seq) >> 31 not in _I32_HIGH:
+        _wide("moe_balance_workspace_bytes")
     return int(lib().moe_balance_workspace_bytes(ctypes.byref(desc), T, n_seq))
 
 
@@ -563,6 +589,8 @@ def _mask(m):
 
 def moe_balance_loss(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_mask, logits, topk_idx, alpha: float,
                      counts, prob_sums, seq_coef, loss, ws, stream=None):
+    if (T | n_seq) >> 31 not in _I32_HIGH:
+        _wide("moe_balance_loss")
     E, k = desc.n_routed, desc.top_k
     d = torch.cuda.current_device()
     _check("moe_balance_loss", lib().moe_balance_loss(
@@ -575,6 +603,8 @@ def moe_balance_loss(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_
 
 def moe_route_backward(desc: MoeLayerDesc, T: int, n_seq: int, seq_offsets, token_mask, logits, topk_idx, counts,
                        seq_coef, d_loss, d_topk_w, d_logits, stream=None):
+    if (T | n_seq) >> 31 not in _I32_HIGH:
+        _wide("moe_route_backward")
     E, k = desc.n_routed, desc.top_k
     d = torch.cuda.current_device()
     _check("moe_route_backward", lib().moe_route_backward(
