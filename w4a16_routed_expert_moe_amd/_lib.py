@@ -200,6 +200,9 @@ def _checked(dev, t, name, dtype, numel, optional=False):
     return p
 
 
+_at = _checked  # until lib() puts the native one in its place: the common case at 0.05 us a tensor instead of 0.3
+
+
 # What the sizes of a call, or-ed, have above 31 bits when each fits an int32
 # (all non-negative, or one negative, which the library refuses): ctypes would
 # cut a wider one to another size than the tensors are checked for.
@@ -210,12 +213,11 @@ def _wide(fn):
     raise ValueError("%s: a size does not fit 32 bits" % fn)
 
 
-_at = _checked  # until lib() puts the native one in its place: the common case at 0.05 us a tensor instead of 0.3
-
-
 # ------------------------------------------------------------------ entry points
 def moe_route(desc: MoeLayerDesc, T: int, x, w_router, gate_bias, logits, topk_idx, topk_w,
               stream=None):
+    if T >> 31 not in _I32_HIGH:
+        _wide("moe_route")
     H, E, k = desc.hidden, desc.n_routed, desc.top_k
     _check("moe_route", lib().moe_route(
         ctypes.byref(desc), T, _ptr(x, "x", torch.bfloat16, T * H),
@@ -226,6 +228,8 @@ def moe_route(desc: MoeLayerDesc, T: int, x, w_router, gate_bias, logits, topk_i
 
 def moe_workspace_bytes(desc: MoeLayerDesc, T: int) -> int:
     """Bytes of the workspace moe_permute / moe_route_permute need at T tokens."""
+    if T >> 31 not in _I32_HIGH:
+        _wide("moe_workspace_bytes")
     return int(lib().moe_workspace_bytes(ctypes.byref(desc), T))
 
 
@@ -238,6 +242,8 @@ def _ws(ws, name="ws"):
 
 def moe_permute(desc: MoeLayerDesc, T: int, topk_idx, group_offsets, sorted_token, row_of_slot,
                 ws=None, stream=None):
+    if T >> 31 not in _I32_HIGH:
+        _wide("moe_permute")
     G, R, S = desc.groups, desc.rows(T), desc.top_k + desc.n_shared
     wp, wb = _ws(ws)
     _check("moe_permute", lib().moe_permute(
@@ -249,6 +255,8 @@ def moe_permute(desc: MoeLayerDesc, T: int, topk_idx, group_offsets, sorted_toke
 
 def moe_route_permute(desc: MoeLayerDesc, T: int, x, w_router, gate_bias, logits, topk_idx, topk_w,
                       group_offsets, sorted_token, row_of_slot, ws, stream=None):
+    if T >> 31 not in _I32_HIGH:
+        _wide("moe_route_permute")
     H, E, k = desc.hidden, desc.n_routed, desc.top_k
     G, R, S = desc.groups, desc.rows(T), desc.top_k + desc.n_shared
     _check("moe_route_permute", lib().moe_route_permute(
@@ -264,6 +272,8 @@ def moe_route_permute(desc: MoeLayerDesc, T: int, x, w_router, gate_bias, logits
 def moe_route_permute_noalloc(desc: MoeLayerDesc, T: int, x, w_router, gate_bias, logits, topk_idx,
                               topk_w, group_offsets, sorted_token, row_of_slot, stream=None):
     """moe_route_permute with the library's own static scratch (no workspace)."""
+    if T >> 31 not in _I32_HIGH:
+        _wide("moe_route_permute_noalloc")
     H, E, k = desc.hidden, desc.n_routed, desc.top_k
     G, R, S = desc.groups, desc.rows(T), desc.top_k + desc.n_shared
     _check("moe_route_permute_noalloc", lib().moe_route_permute_noalloc(
@@ -278,6 +288,8 @@ def moe_route_permute_noalloc(desc: MoeLayerDesc, T: int, x, w_router, gate_bias
 
 def moe_w4a16_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_gather, n_src: int, a_sums, N: int, K: int,
                            w_packed, w_scales, group_offsets, act: int, out, stream=None):
+    if (T | N | K | act) >> 31 not in _I32_HIGH or n_src >> 31 not in _I32_HIGH:
+        _wide("moe_w4a16_grouped_gemm")
     G, R = desc.groups, desc.rows(T)
     a_rows = n_src if a_gather is not None else R
     out_cols = N // 2 if act == MOE_ACT_SWIGLU else N
@@ -293,6 +305,8 @@ def moe_w4a16_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_gather, n_src: int, 
 
 def moe_mxfp4_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_gather, n_src: int, N: int, K: int,
                            w_packed, w_scales, group_offsets, act: int, out, stream=None):
+    if (T | N | K | act) >> 31 not in _I32_HIGH or n_src >> 31 not in _I32_HIGH:
+        _wide("moe_mxfp4_grouped_gemm")
     G, R = desc.groups, desc.rows(T)
     a_rows = n_src if a_gather is not None else R
     out_cols = N // 2 if act == MOE_ACT_SWIGLU else N
@@ -306,6 +320,8 @@ def moe_mxfp4_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_gather, n_src: int, 
 
 
 def moe_row_sums(rows: int, K: int, a, sums, stream=None):
+    if (rows | K) >> 31 not in _I32_HIGH:
+        _wide("moe_row_sums")
     _check("moe_row_sums", lib().moe_row_sums(
         rows, K, _ptr(a, "a", torch.bfloat16, rows * K),
         _ptr(sums, "sums", torch.float32, rows * (K // 128)), _stream(stream)))
@@ -313,6 +329,8 @@ def moe_row_sums(rows: int, K: int, a, sums, stream=None):
 
 def moe_w4a16_down_combine(desc: MoeLayerDesc, T: int, h, w_packed, w_scales, topk_idx, topk_w,
                            row_of_slot, out, stream=None):
+    if T >> 31 not in _I32_HIGH:
+        _wide("moe_w4a16_down_combine")
     H, I, G, R, S = desc.hidden, desc.inter, desc.groups, desc.rows(T), desc.top_k + desc.n_shared
     _check("moe_w4a16_down_combine", lib().moe_w4a16_down_combine(
         ctypes.byref(desc), T, _ptr(h, "h", torch.bfloat16, R * I),
@@ -388,6 +406,8 @@ def moe_w4a16_decode_token_supported(desc: MoeLayerDesc) -> int:
 
 
 def moe_combine(desc: MoeLayerDesc, T: int, y, row_of_slot, topk_w, out, stream=None):
+    if T >> 31 not in _I32_HIGH:
+        _wide("moe_combine")
     H, R, S = desc.hidden, desc.rows(T), desc.top_k + desc.n_shared
     _check("moe_combine", lib().moe_combine(
         ctypes.byref(desc), T, _ptr(y, "y", torch.bfloat16, R * H),
@@ -397,6 +417,8 @@ def moe_combine(desc: MoeLayerDesc, T: int, y, row_of_slot, topk_w, out, stream=
 
 
 def moe_w4a16_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stream=None):
+    if (n_groups | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_w4a16_prepack")
     n = n_groups * N * K // 2
     _check("moe_w4a16_prepack", lib().moe_w4a16_prepack(
         n_groups, N, K, _ptr(w_canonical, "w_canonical", torch.uint8, n),
@@ -404,6 +426,8 @@ def moe_w4a16_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stre
 
 
 def moe_mxfp4_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stream=None):
+    if (n_groups | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_mxfp4_prepack")
     n = n_groups * N * K // 2
     _check("moe_mxfp4_prepack", lib().moe_mxfp4_prepack(
         n_groups, N, K, _ptr(w_canonical, "w_canonical", torch.uint8, n),
@@ -412,6 +436,8 @@ def moe_mxfp4_prepack(n_groups: int, N: int, K: int, w_canonical, w_packed, stre
 
 def moe_gen_ue8m0_scales(seed: int, layer: int, group0: int, n_groups: int, kind: int, N: int, K: int,
                          out, stream=None):
+    if (n_groups | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_gen_ue8m0_scales")
     _check("moe_gen_ue8m0_scales", lib().moe_gen_ue8m0_scales(
         seed, layer, group0, n_groups, kind, N, K,
         _ptr(out, "out", torch.uint8, n_groups * N * (K // 32)), _stream(stream)))
@@ -419,6 +445,8 @@ def moe_gen_ue8m0_scales(seed: int, layer: int, group0: int, n_groups: int, kind
 
 def moe_gen_int4_codes(seed: int, layer: int, group0: int, n_groups: int, kind: int, N: int, K: int,
                        out, stream=None):
+    if (n_groups | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_gen_int4_codes")
     _check("moe_gen_int4_codes", lib().moe_gen_int4_codes(
         seed, layer, group0, n_groups, kind, N, K,
         _ptr(out, "out", torch.uint8, n_groups * N * K // 2), _stream(stream)))
@@ -426,6 +454,8 @@ def moe_gen_int4_codes(seed: int, layer: int, group0: int, n_groups: int, kind: 
 
 def moe_gen_fp16_scales(seed: int, layer: int, group0: int, n_groups: int, kind: int, N: int, K: int,
                         out, stream=None):
+    if (n_groups | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_gen_fp16_scales")
     _check("moe_gen_fp16_scales", lib().moe_gen_fp16_scales(
         seed, layer, group0, n_groups, kind, N, K,
         _ptr(out, "out", torch.float16, n_groups * N * (K // 128)), _stream(stream)))
@@ -441,12 +471,16 @@ def moe_abi_version() -> int:
 
 # ------------------------------------------------------------------ fp8 activations
 def moe_act_quant_fp8(rows: int, K: int, a, codes, scales, stream=None):
+    if (rows | K) >> 31 not in _I32_HIGH:
+        _wide("moe_act_quant_fp8")
     _check("moe_act_quant_fp8", lib().moe_act_quant_fp8(
         rows, K, _ptr(a, "a", torch.bfloat16, rows * K), _ptr(codes, "codes", torch.uint8, rows * K),
         _ptr(scales, "scales", torch.uint8, rows * (K // 128)), _stream(stream)))
 
 
 def moe_act_quant_fp8_dequant(rows: int, K: int, a, codes, scales, deq, stream=None):
+    if (rows | K) >> 31 not in _I32_HIGH:
+        _wide("moe_act_quant_fp8_dequant")
     _check("moe_act_quant_fp8_dequant", lib().moe_act_quant_fp8_dequant(
         rows, K, _ptr(a, "a", torch.bfloat16, rows * K), _ptr(codes, "codes", torch.uint8, rows * K),
         _ptr(scales, "scales", torch.uint8, rows * (K // 128)), _ptr(deq, "deq", torch.bfloat16, rows * K),
@@ -455,6 +489,8 @@ def moe_act_quant_fp8_dequant(rows: int, K: int, a, codes, scales, deq, stream=N
 
 def moe_w4a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_src: int, N: int, K: int,
                           w_packed, w_scales, group_offsets, act: int, out, stream=None):
+    if (T | N | K | act) >> 31 not in _I32_HIGH or n_src >> 31 not in _I32_HIGH:
+        _wide("moe_w4a8_grouped_gemm")
     G, R = desc.groups, desc.rows(T)
     a_rows = n_src if a_gather is not None else R
     out_cols = N // 2 if act == MOE_ACT_SWIGLU else N
@@ -469,6 +505,8 @@ def moe_w4a8_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_s
 
 
 def moe_fp8_block_gemm(M: int, N: int, K: int, a, a_scales, w_packed, w_scales, out, stream=None):
+    if (M | N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_fp8_block_gemm")
     _check("moe_fp8_block_gemm", lib().moe_fp8_block_gemm(
         M, N, K, _ptr(a, "a", torch.uint8, M * K), _ptr(a_scales, "a_scales", torch.uint8, M * (K // 128)),
         _ptr(w_packed, "w_packed", torch.uint8, N * K),
@@ -477,6 +515,8 @@ def moe_fp8_block_gemm(M: int, N: int, K: int, a, a_scales, w_packed, w_scales, 
 
 
 def moe_fp8_prepack(N: int, K: int, w_canonical, w_packed, stream=None):
+    if (N | K) >> 31 not in _I32_HIGH:
+        _wide("moe_fp8_prepack")
     _check("moe_fp8_prepack", lib().moe_fp8_prepack(
         N, K, _ptr(w_canonical, "w_canonical", torch.uint8, N * K), _ptr(w_packed, "w_packed", torch.uint8, N * K),
         _stream(stream)))
