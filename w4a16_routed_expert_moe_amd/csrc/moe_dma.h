@@ -15,10 +15,12 @@ __device__ __forceinline__ i32x4 buffer(const char *p, int64_t bytes) {
     return i32x4{(int)(uint32_t)(uintptr_t)p, (int)((uintptr_t)p >> 32), n, 0x00027000};
 }
 // 16 bytes per lane straight into LDS, from a buffer or from an address each
-// (see dma16_untracked; M0 is not restored: nothing else here reads it).
+// (see dma16_untracked, also for the wait state; M0 is not restored: nothing
+// else here reads it).
 __device__ __forceinline__ void dma16_buffer(i32x4 r, uint32_t voff, uint32_t soff, uint32_t lds) {
     asm volatile(
         "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
         "buffer_load_dwordx4 %0, %1, %3 offen lds"
         :
         : "v"(voff), "s"(r), "s"(lds), "s"(soff)
@@ -27,6 +29,7 @@ __device__ __forceinline__ void dma16_buffer(i32x4 r, uint32_t voff, uint32_t so
 __device__ __forceinline__ void dma16_pointer(uint64_t src, uint32_t lds) {
     asm volatile(
         "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dwordx4 %0, off"
         :
         : "v"(src), "s"(lds)

@@ -44,6 +44,7 @@ __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ void dma4_pointer(uint64_t src, uint32_t lds) {  // 4 bytes a lane (see dma16_pointer)
     asm volatile(
         "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dword %0, off"
         :
         : "v"(src), "s"(lds)
@@ -52,6 +53,7 @@ __device__ __forceinline__ void dma4_pointer(uint64_t src, uint32_t lds) {  // 4
 __device__ __forceinline__ void dma4_buffer(i32x4 r, uint32_t voff, uint32_t soff, uint32_t lds) {
     asm volatile(
         "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
         "buffer_load_dword %0, %1, %3 offen lds"
         :
         : "v"(voff), "s"(r), "s"(lds), "s"(soff)

@@ -69,6 +69,8 @@ __device__ __forceinline__ void dma16(const void *g, void *lds) {
 // pass does not track.  Tracked, they make the pass wait for every load into LDS before the
 // first LDS read that follows them, however far ahead they were issued; the
 // kernels order their completion with explicit waits instead.
+// The instruction between the write of M0 and the load is the wait state that
+// the hardware wants there; the compiler does not see into the assembly to add it.
 // M0 is a reserved register, so the assembly restores it: to the compiler
 // it is unchanged.
 __device__ __forceinline__ void dma16_untracked(const void *g, void *lds) {
@@ -77,6 +79,7 @@ __device__ __forceinline__ void dma16_untracked(const void *g, void *lds) {
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dwordx4 %1, off\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)

@@ -57,6 +57,7 @@ __device__ __forceinline__ void dma16_untracked_sv(gchar_ptr base, uint32_t voff
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %3\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dwordx4 %1, %2\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)
@@ -69,6 +70,7 @@ __device__ __forceinline__ void dma4_untracked_sv(gchar_ptr base, uint32_t voff,
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %3\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dword %1, %2\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)
@@ -83,6 +85,7 @@ __device__ __forceinline__ void dma4_untracked(const void *g, void *lds) {
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
         "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
         "global_load_lds_dword %1, off\n\t"
         "s_mov_b32 m0, %0"
         : "=&s"(saved)
