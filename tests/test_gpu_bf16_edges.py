@@ -1,0 +1,151 @@
+"""What lies beside an operand of the bf16 products does not reach their results: rows, weights and columns that are not
+finite, next to where a group, a row or the contraction ends inside a tile.
+
+The tiles fill up with zeros past the end of a group; whatever is read there instead is multiplied by the zeros of the
+other operand, which hides every finite value and shows an infinity or a NaN.  Inputs are small integers, so that the
+results of the finite groups are compared bit for bit (see test_gpu_bf16.py)."""
+import pytest
+import torch
+
+import w4a16_routed_expert_moe_amd as moe
+from gpu_common import say
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+BAD = (float("nan"), float("inf"), -float("inf"))
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _ints(gen, *shape):
+    return torch.randint(-4, 5, shape, device="cuda", generator=gen).to(BF16)
+
+
+def _bad(gen, *shape):
+    return torch.tensor(BAD, dtype=BF16, device="cuda")[torch.randint(0, 3, shape, device="cuda", generator=gen)]
+
+
+def _offsets(sizes):
+    return torch.tensor([0] + sizes, dtype=torch.int32).cumsum(0).to(torch.int32)
+
+
+def _desc(G):
+    return moe.MoeLayerDesc.make(512, 128, G, 1, 0)
+
+
+def _gather(gen, n, on):
+    """A gather of n rows from n + 3 sources (a permutation, three of them unused), or None."""
+    return torch.randperm(n + 3, device="cuda", generator=gen)[:n].to(torch.int32) if on else None
+
+
+def _source(rows, gather):
+    """The tensor that `gather` reads as rows."""
+    if gather is None:
+        return rows
+    a = torch.full((len(rows) + 3, rows.shape[1]), float("nan"), dtype=BF16, device="cuda")
+    a[gather.long()] = rows
+    return a
+
+
+# groups that end inside a step of 64 rows, the first row of every other group and all that follow in it not finite
+SHORT = [17, 9, 1, 30, 63, 64, 65, 3, 40, 129, 100, 16]
+
+
+@pytest.mark.parametrize("mode", [moe.MOE_GRAD_BF16, moe.MOE_GRAD_F32, moe.MOE_GRAD_F32_ADD])
+@pytest.mark.parametrize("which", ["dy", "a", None])
+@pytest.mark.parametrize("N,K", [(80, 48), (272, 400), (16, 1040), (3600, 4096)])  # the last: tiles of 256 x 256
+def test_rows_of_the_next_group(N, K, which, mode):
+    say("wgrad N=%d K=%d gathered %s mode %d" % (N, K, which, mode))
+    gen, G, R = _gen(N + K), len(SHORT), sum(SHORT)
+    if N > 1000:  # as launch_wide counts them
+        assert G * -(-N // 256) * -(-K // 256) >= 2048
+    off = _offsets(SHORT)
+    odd = torch.zeros(R, dtype=torch.bool, device="cuda")
+    for g in range(1, G, 2):
+        odd[off[g]:off[g + 1]] = True
+    rows = {"dy": _ints(gen, R, N), "a": _ints(gen, R, K)}
+    for t in rows.values():
+        t[odd] = _bad(gen, int(odd.sum()), t.shape[1])
+    gather = _gather(gen, R, which is not None)
+    at = {n: gather if n == which else None for n in rows}
+    kind = BF16 if mode == moe.MOE_GRAD_BF16 else torch.float32
+    dw = torch.full((G, N, K), 3.0, dtype=kind, device="cuda")
+    moe.moe_bf16_grouped_wgrad(_desc(G), R, _source(rows["dy"], at["dy"]), at["dy"], _source(rows["a"], at["a"]), at["a"], R + 3, N, K,
+                               off.cuda(), mode, dw)
+    torch.cuda.synchronize()
+    for g in range(0, G, 2):
+        r = slice(int(off[g]), int(off[g + 1]))
+        want = torch.matmul(rows["dy"][r].double().t(), rows["a"][r].double())
+        if mode == moe.MOE_GRAD_F32_ADD:
+            want += 3.0
+        assert torch.equal(dw[g], want.float().to(kind)), g
+    for g in range(1, G, 2):
+        assert not torch.isfinite(dw[g]).any(), g
+
+
+# rows a group, output columns: tiles of 64 x 128, 128 x 128 and 256 x 256
+@pytest.mark.parametrize("rows,K", [(10, 272), (70, 400), (500, 9040)])
+@pytest.mark.parametrize("N", [16, 48, 80, 176, 272])
+@pytest.mark.parametrize("gather", [True, False])
+def test_weights_of_the_next_group(rows, K, N, gather):
+    say("dgrad %d rows N=%d K=%d" % (rows, N, K))
+    sizes = [rows, rows + 1, rows - 3, rows + 5, rows + 17, rows]
+    gen, G, R = _gen(N + K), len(sizes), sum(sizes)
+    if rows == 500:
+        assert R >= 128 * G and (-(-R // 256) + G // 2) * -(-K // 256) >= 512
+    off = _offsets(sizes)
+    w, dy = _ints(gen, G, N, K), _ints(gen, R, N)
+    w[1::2] = _bad(gen, *w[1::2].shape)
+    at = _gather(gen, R, gather)
+    da = torch.empty((R, K), dtype=BF16, device="cuda")
+    moe.moe_bf16_grouped_dgrad(_desc(G), R, _source(dy, at), at, R + 3, N, K, w, off.cuda(), da)
+    torch.cuda.synchronize()
+    for g in range(G):
+        r = slice(int(off[g]), int(off[g + 1]))
+        if g % 2:
+            assert not torch.isfinite(da[r]).all(0).any(), g
+        else:
+            assert torch.equal(da[r], torch.matmul(dy[r].double(), w[g].double()).float().to(BF16)), g
+
+
+def _silu(g):
+    return g / (1 + torch.exp(-g))
+
+
+# rows of each group, columns, k: the stream, tiles of 64 x 256 (64 MB of weights), of 64 x 128, 128 x 128 and 256 x 256
+@pytest.mark.parametrize("sizes,N,K", [([2, 0, 1, 3], 96, 80), ([20] * 33, 1056, 1040), ([21] * 24, 288, 144), ([70, 65, 60, 80], 288, 208),
+                                       ([700, 801, 650, 705], 8224, 336)])
+@pytest.mark.parametrize("act", [moe.MOE_ACT_NONE, moe.MOE_ACT_SWIGLU])
+def test_the_next_row_of_weights_and_of_tokens(sizes, N, K, act):
+    """Every other weight row and every third token not finite: the columns and rows between them do not see it."""
+    say("forward %d groups N=%d K=%d act %d" % (len(sizes), N, K, act))
+    gen, G, R = _gen(N + K), len(sizes), sum(sizes)
+    off = _offsets(sizes)
+    w, a = _ints(gen, G, N, K), _ints(gen, R, K)
+    w *= 0.25
+    good = torch.arange(0, N, 2, device="cuda")
+    w[:, 1::2] = _bad(gen, *w[:, 1::2].shape)
+    bad_row = torch.arange(R, device="cuda") % 3 == 1
+    a[bad_row] = _bad(gen, int(bad_row.sum()), K)
+    C = N // 2 if act == moe.MOE_ACT_SWIGLU else N
+    out = torch.empty((R, C), dtype=BF16, device="cuda")
+    moe.moe_bf16_grouped_gemm(_desc(G), R, a, None, 0, N, K, w, off.cuda(), act, None, out)
+    torch.cuda.synchronize()
+    for g in range(G):
+        r = torch.arange(int(off[g]), int(off[g + 1]), device="cuda")
+        r = r[~bad_row[r]]
+        z = torch.matmul(a[r].double(), w[g][good].double().t())
+        got = out[r][:, :C:2]
+        if act == moe.MOE_ACT_NONE:
+            assert torch.equal(got, z.float().to(BF16)), g
+        else:  # half a step of bf16, and e^-g, the reciprocal and the products in fp32 (see test_gpu_bf16.py)
+            gate, up = z[:, :C // 2], z[:, C // 2:]
+            want = _silu(gate) * up
+            tol = want.abs() * (2.0 ** -8 + (2 * gate.abs() + 8) * 2.0 ** -23) + 2.0 ** -133
+            assert (((got.double() - want).abs() <= tol) | (gate < -80)).all(), g
+        assert not torch.isfinite(out[r][:, 1:C:2]).any(), g

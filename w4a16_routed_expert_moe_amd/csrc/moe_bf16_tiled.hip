@@ -28,14 +28,15 @@ constexpr int kBK = 64;  // contraction per step
 // What lanes without an element of a row load.
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 
-// A buffer of at most kFar bytes from p: loads from past its end give zeros.
+// A buffer of at most kFar bytes from p: loads from past its end give zeros (no
+// part of an offset is scalar, see moe_dma.h).
 constexpr uint32_t kFar = 0x3FFFFFFFu;
 __device__ __forceinline__ rsrc_t buffer(const void *p, int64_t bytes) {
     const int n = bytes < 0 ? 0 : bytes > (int64_t)kFar ? (int)kFar : (int)bytes;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, n, 0x00027000);
 }
-__device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t voff, uint32_t soff) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+__device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t voff) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, 0, 0));
 }
 // s_waitcnt immediate: at most n vector loads outstanding, no LDS operation.
 constexpr int wait_imm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0070; }
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(256, 2) void k_bf16_tiled(Args p) {
         const int j = i >> 1;
         const uint32_t far = kBK * kg + 16 * q >= K ? kFar : 0u;  // past the row's end: zeros
         const bool u = EPI == kSwiglu && j >= HS;
-        part[i] = load16(u ? b1 : b0, voff + 16 * (i & 1) + far, (uint32_t)((u ? j - HS : j) * ld) + 128 * kg);
+        part[i] = load16(u ? b1 : b0, voff + 16 * (i & 1) + far + (uint32_t)((u ? j - HS : j) * ld) + 128 * kg);
     };
     u32x4 raw[2][2 * NSW];  // of two steps
     constexpr int PFD = 3, WIN = 4;  // m-tiles that an operand read is ahead of its use

@@ -260,14 +260,14 @@ __device__ __forceinline__ void multiply(const Args &p, int block, char *stages)
         if constexpr (!TRB) {
             const int r = 8 * (NW * wave + j);  // (the swizzle goes by its place in 64 rows)
             const int x = NW == 8 ? j >> 1 : (2 * wave + (j >> 1)) & 3;
-            uint32_t voff = NW == 8 ? boff[j >> 1] : (wave & 1) ? boff[2 + (j >> 1)] : boff[j >> 1];
-            if (cut && kBK * kg + 8 * ((l & 7) ^ wswz(16 * x + (l >> 3))) >= KC) voff = kFar;
             const bool u = EPI == kSwiglu && NW == 4 && (j & 1);
             const int row = EPI == kSwiglu && NW == 4 ? 8 * (j >> 1) : 8 * j;
-            dma16_buffer(u ? ubuf : bbuf, voff, (uint32_t)(row * ld) + 128 * kg, lds + 128 * r);
+            uint32_t voff = (NW == 8 ? boff[j >> 1] : (wave & 1) ? boff[2 + (j >> 1)] : boff[j >> 1]) + (uint32_t)(row * ld) + 128 * kg;
+            if (cut && kBK * kg + 8 * ((l & 7) ^ wswz(16 * x + (l >> 3))) >= KC) voff = kFar;
+            dma16_buffer(u ? ubuf : bbuf, voff, lds + 128 * r);
         } else {
             if (j == 0) bbuf = buffer(bbase + (size_t)kg * kBK * ld, bbytes - (int64_t)kg * kBK * ld);
-            dma16_buffer(bbuf, boff[0], (uint32_t)(stage_row(kCols, j, 0) * ld), lds + 2 * kCols * stage_row(kCols, j, wave));
+            dma16_buffer(bbuf, boff[0] + (uint32_t)(stage_row(kCols, j, 0) * ld), lds + 2 * kCols * stage_row(kCols, j, wave));
         }
     };
 

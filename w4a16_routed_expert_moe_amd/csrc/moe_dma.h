@@ -8,7 +8,9 @@ namespace moe {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// A buffer of at most kFar bytes from p: loads from past its end give zeros.
+// A buffer of at most kFar bytes from p.  A load gives zeros where its lane
+// offset is not below the buffer's size less the scalar offset, which therefore
+// must not lie past the end itself: offsets that may are all in the lanes.
 constexpr uint32_t kFar = 0x3FFFFFFFu;
 __device__ __forceinline__ i32x4 buffer(const char *p, int64_t bytes) {
     const int n = bytes < 0 ? 0 : bytes > (int64_t)kFar ? (int)kFar : (int)bytes;
@@ -24,6 +26,15 @@ __device__ __forceinline__ void dma16_buffer(i32x4 r, uint32_t voff, uint32_t so
         "buffer_load_dwordx4 %0, %1, %3 offen lds"
         :
         : "v"(voff), "s"(r), "s"(lds), "s"(soff)
+        : "memory");
+}
+__device__ __forceinline__ void dma16_buffer(i32x4 r, uint32_t voff, uint32_t lds) {
+    asm volatile(
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %0, %1, 0 offen lds"
+        :
+        : "v"(voff), "s"(r), "s"(lds)
         : "memory");
 }
 __device__ __forceinline__ void dma16_pointer(uint64_t src, uint32_t lds) {

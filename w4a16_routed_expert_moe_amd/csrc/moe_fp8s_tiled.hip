@@ -50,13 +50,13 @@ __device__ __forceinline__ void dma4_pointer(uint64_t src, uint32_t lds) {  // 4
         : "v"(src), "s"(lds)
         : "memory");
 }
-__device__ __forceinline__ void dma4_buffer(i32x4 r, uint32_t voff, uint32_t soff, uint32_t lds) {
+__device__ __forceinline__ void dma4_buffer(i32x4 r, uint32_t voff, uint32_t lds) {
     asm volatile(
         "s_mov_b32 m0, %2\n\t"
         "s_nop 0\n\t"
-        "buffer_load_dword %0, %1, %3 offen lds"
+        "buffer_load_dword %0, %1, 0 offen lds"
         :
-        : "v"(voff), "s"(r), "s"(lds), "s"(soff)
+        : "v"(voff), "s"(r), "s"(lds)
         : "memory");
 }
 
@@ -176,15 +176,16 @@ __global__ __launch_bounds__(64 * WM * WN * KS, OCC) void k_fp8s_tiled(Args p) {
 #pragma unroll
     for (int i = 0; i < MW; ++i) live |= (uint32_t)(sRow[16 * (WM * i + wm) + m] >= 0) << i;
     // the scales of steps [8 kg8, 8 kg8 + 8); those past the last block are not used
+    // (they may lie past the buffers' ends, so that none of the offset is scalar)
     auto load_scales = [&](int kg8) {
-        if (wm == 0 && l < 16) dma4_buffer(wbuf, wsrc, 32 * KS * kg8, ldsW + (kg8 & 1) * 64);
+        if (wm == 0 && l < 16) dma4_buffer(wbuf, wsrc + 32 * KS * kg8, ldsW + (kg8 & 1) * 64);
 #pragma unroll
         for (int i = 0; i < LS; ++i) {
             const uint32_t to = __builtin_amdgcn_readfirstlane(ldsS + (kg8 & 1) * (TM * 32) + 256 * (i * NW + wave));
             if constexpr (FAR)
                 dma4_pointer(ssrc[i] + 4 * min((8 * kg8 + sblock(i)) * KS + ks, KG - 1), to);
             else
-                dma4_buffer(sbuf, ssrc[i], 32 * KS * kg8, to);
+                dma4_buffer(sbuf, ssrc[i] + 32 * KS * kg8, to);
         }
     };
     // load x of step kg into stage s; past the end of the rows: zeros
