@@ -88,6 +88,31 @@ def test_rows_of_the_next_group(N, K, which, mode):
         assert not torch.isfinite(dw[g]).any(), g
 
 
+@pytest.mark.parametrize("mode", [moe.MOE_GRAD_BF16, moe.MOE_GRAD_F32])
+@pytest.mark.parametrize("which", ["dy", "a"])
+@pytest.mark.parametrize("N,K", [(80, 48), (272, 400), (3600, 4096)])
+def test_rows_without_a_source_add_nothing(N, K, which, mode):
+    """... whatever the other operand holds in them."""
+    gen, G, R = _gen(N - K), len(SHORT), sum(SHORT)
+    off = _offsets(SHORT)
+    rows = {"dy": _ints(gen, R, N), "a": _ints(gen, R, K)}
+    none = torch.arange(R, device="cuda") % 5 == 2
+    for t in rows.values():
+        t[none] = _bad(gen, int(none.sum()), t.shape[1])
+    at = _gather(gen, R, True)
+    source = _source(rows[which], at)
+    at[none] = torch.tensor([-1, R + 3, -(1 << 31), (1 << 31) - 1], dtype=torch.int32, device="cuda")[torch.arange(int(none.sum()), device="cuda") % 4]
+    given = {n: (source, at) if n == which else (t, None) for n, t in rows.items()}
+    kind = BF16 if mode == moe.MOE_GRAD_BF16 else torch.float32
+    dw = torch.empty((G, N, K), dtype=kind, device="cuda")
+    moe.moe_bf16_grouped_wgrad(_desc(G), R, *given["dy"], *given["a"], R + 3, N, K, off.cuda(), mode, dw)
+    torch.cuda.synchronize()
+    for g in range(G):
+        r = torch.arange(int(off[g]), int(off[g + 1]), device="cuda")
+        r = r[~none[r]]
+        assert torch.equal(dw[g], torch.matmul(rows["dy"][r].double().t(), rows["a"][r].double()).float().to(kind)), g
+
+
 # rows a group, output columns: tiles of 64 x 128, 128 x 128 and 256 x 256
 @pytest.mark.parametrize("rows,K", [(10, 272), (70, 400), (500, 9040)])
 @pytest.mark.parametrize("N", [16, 48, 80, 176, 272])

@@ -267,7 +267,12 @@ __device__ __forceinline__ void multiply(const Args &p, int block, char *stages)
             dma16_buffer(u ? ubuf : bbuf, voff, lds + 128 * r);
         } else {
             if (j == 0) bbuf = buffer(bbase + (size_t)kg * kBK * ld, bbytes - (int64_t)kg * kBK * ld);
-            dma16_buffer(bbuf, boff[0] + (uint32_t)(stage_row(kCols, j, 0) * ld), lds + 2 * kCols * stage_row(kCols, j, wave));
+            uint32_t voff = boff[0] + (uint32_t)(stage_row(kCols, j, 0) * ld);
+            if constexpr (FORM == kTN) {  // a row that a has no source for adds nothing, whatever b has there
+                static_assert(TM == kCols, "load j brings the same rows of both");
+                if ((unsigned)arow[j] >= (unsigned)n_rows) voff = kFar;
+            }
+            dma16_buffer(bbuf, voff, lds + 2 * kCols * stage_row(kCols, j, wave));
         }
     };
 
