@@ -174,3 +174,48 @@ def test_the_next_row_of_weights_and_of_tokens(sizes, N, K, act):
             tol = want.abs() * (2.0 ** -8 + (2 * gate.abs() + 8) * 2.0 ** -23) + 2.0 ** -133
             assert (((got.double() - want).abs() <= tol) | (gate < -80)).all(), g
         assert not torch.isfinite(out[r][:, 1:C:2]).any(), g
+
+
+@pytest.mark.parametrize("which", ["dy", "a", None])
+@pytest.mark.parametrize("N,K", [(80, 48), (3600, 4096)])
+def test_gradients_of_groups_without_rows_are_not_touched(N, K, which):
+    """Added to, the fp32 gradient of a group without rows keeps its bits (a minus zero with zero added would be plus zero)."""
+    sizes = [0, 40, 0, 0, 7, 0, 70, 0, 0]
+    gen, G, R = _gen(N), len(sizes), sum(sizes)
+    rows = {"dy": _ints(gen, R, N), "a": _ints(gen, R, K)}
+    gather = _gather(gen, R, which is not None)
+    at = {n: gather if n == which else None for n in rows}
+    dw = torch.full((G, N, K), -0.0, device="cuda")
+    moe.moe_bf16_grouped_wgrad(_desc(G), R, _source(rows["dy"], at["dy"]), at["dy"], _source(rows["a"], at["a"]), at["a"], R + 3, N, K,
+                               _offsets(sizes).cuda(), moe.MOE_GRAD_F32_ADD, dw)
+    torch.cuda.synchronize()
+    off = _offsets(sizes)
+    for g in range(G):
+        if not sizes[g]:
+            assert (dw[g].view(torch.int32) == -(1 << 31)).all(), g
+        else:
+            r = slice(int(off[g]), int(off[g + 1]))
+            assert torch.equal(dw[g], torch.matmul(rows["dy"][r].double().t(), rows["a"][r].double()).float()), g
+
+
+@pytest.mark.parametrize("T", [6, 300])
+def test_backward_does_not_touch_the_gradients_of_idle_experts(T):
+    """The same of the whole backward pass (few tiles: all gradients in one launch; and each in its own)."""
+    H, I, E, k = (512, 128, 24, 1) if T == 6 else (4096, 2048, 9, 1)
+    gen = _gen(T)
+    desc = moe.MoeLayerDesc.make(H, I, E, k, 0)
+    buf = moe.Buffers(desc, T, train=True)
+    idx = torch.arange(T, dtype=torch.int32, device="cuda")[:, None] % 3 * 2 + 1  # experts 1, 3 and 5
+    moe.moe_permute(desc, T, idx, buf.group_offsets, buf.sorted_token, buf.row_of_slot, buf.ws)
+    x, d_out = (torch.randn((T, H), device="cuda", generator=gen).to(BF16) for _ in range(2))
+    w13 = (torch.randn((E, 2 * I, H), device="cuda", generator=gen) / H ** 0.5).to(BF16)
+    w2 = (torch.randn((E, H, I), device="cuda", generator=gen) / I ** 0.5).to(BF16)
+    buf.topk_w.fill_(0.5)
+    d13, d2 = (torch.full(w.shape, -0.0, device="cuda") for w in (w13, w2))
+    moe.moe_bf16_experts(desc, T, x, buf.topk_w, buf.group_offsets, buf.sorted_token, buf.row_of_slot, w13, w2, buf.gu, buf.h, buf.y, buf.out)
+    moe.moe_bf16_experts_backward(desc, T, d_out, x, buf.topk_w, buf.group_offsets, buf.sorted_token, buf.row_of_slot, w13, w2, buf.gu,
+                                  buf.h, moe.MOE_GRAD_F32_ADD, buf.d_x, d13, d2, buf.d_topk_w, buf.grad_ws)
+    torch.cuda.synchronize()
+    for e in range(E):
+        for d in (d13, d2):
+            assert (d[e] != 0).any() if e in (1, 3, 5) else (d[e].view(torch.int32) == -(1 << 31)).all(), e

@@ -175,6 +175,7 @@ __device__ __forceinline__ void multiply(const Args &p, int block, char *stages)
     Item it;
     if (!find_item<FORM>(p, block, TM, it)) return;
     const int KC = FORM == kTN ? max(it.hi - it.lo, 0) : p.K;  // contraction
+    if (EPI == kAddF32 && KC == 0) return;  // a group without rows: its gradient stays as it is
     const int KG = (KC + kBK - 1) / kBK;
     // columns of the tile: of the output, or (SwiGLU) half of them of the gate
     // projection and the same of the up projection
