@@ -477,7 +477,10 @@ bool launch_tiled(int act, Args a, hipStream_t st) {
     // 4096 x 4096, would be 974 -> 1259.
     const bool exact = swiglu && (int64_t)a.R * a.N <= 1 << 23;
     if (a.gather && (int64_t)a.n_src * a.K > kNone) {
-        swiglu ? launch<kSilu, 2, 2, 2, 1, 3, true>(a, st) : launch<kPlain, 2, 2, 2, 1, 3, true>(a, st);
+        if (exact)
+            launch<kSilu, 2, 2, 2, 1, 2, true, true>(a, st);
+        else
+            swiglu ? launch<kSilu, 2, 2, 2, 1, 3, true>(a, st) : launch<kPlain, 2, 2, 2, 1, 3, true>(a, st);
     } else if (a.R >= 128 * G && tiles(256, 256) >= 256 && !exact) {
         if (swiglu && a.hq) {
             launch<kSilu, 8, 2, 4, 1, 2, false, false, true>(a, st);
