@@ -578,10 +578,18 @@ moe_status moe_w8a8_experts(const moe_layer_desc *desc, int32_t T, const uint16_
 /* of two, and moe_w8a8_*.  With b the blocks of 128 k (the last one may be  */
 /* shorter), KG = ceil(K/128):                                               */
 /*   out[m][n] = bf16( sum_b a_scales[m][b] w_scales[n/128][b] *             */
-/*                     sum_{k in b} a[m][k] w[n][k] )       (fp32 sums)      */
+/*                     sum_{k in b} a[m][k] w[n][k] )                        */
 /* The two scales are multiplied first, in fp32: where that product leaves   */
-/* fp32's range the output does too, or loses digits.  Outputs and scratch   */
-/* overlap neither each other nor an input.                                  */
+/* fp32's range the output does too, or loses digits.  The sums over the     */
+/* blocks are fp32 ones.  Those over the k of a block are the fp8 matrix     */
+/* instruction's: of eight k (8i..8i+7) each product is cut off at 2^-13 of  */
+/* the largest one's power of two (up to 7 * 2^-13 of the largest lost), then */
+/* they are added in fp32.  Before SwiGLU the products are bf16 ones, whose  */
+/* sums are fp32 throughout (a cut at 2^-24 there), where T <= 64 or R*N <=   */
+/* 2^23, so that h, which is quantised again, is the one of fp32 sums there. */
+/* A token's outputs may differ in their last bits with the size of its batch */
+/* (other tiles add in another order), and, past these bounds, by the cut.    */
+/* Outputs and scratch overlap neither each other nor an input.               */
 
 /* Quantisation of each 128 elements of a row by themselves: with amax the   */
 /* largest |a| of the block,                                                 */

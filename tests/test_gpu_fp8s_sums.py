@@ -51,6 +51,37 @@ def _weights(codes, scales):
     return codes.view(F8).double() * scales.double().repeat_interleave(128, -1)[..., :K].repeat_interleave(128, -2)[..., :N, :]
 
 
+# ---------------------------------------------------------------- the bound of the fp8 instruction
+@pytest.mark.parametrize("values", ["any", "one large in eight", "integers that cancel"])
+@pytest.mark.parametrize("M,N,K", [(1, 16, 16), (3, 144, 16), (16, 64, 144), (40, 272, 400), (130, 80, 1040), (64, 4096, 144), (300, 528, 272)])
+def test_products_within_their_bound(M, N, K, values):
+    say("M=%d N=%d K=%d %s" % (M, N, K, values))
+    gen = _gen(M + N + K)
+    NB, KB = _nk(N, K)
+    a, w = (torch.randint(0, 256, s, dtype=torch.uint8, device="cuda", generator=gen) for s in ((M, K), (N, K)))
+    if values == "one large in eight":
+        for t in (a, w):
+            t[:] = (t & 0x80) | 0x28 + (t & 15)  # 2^-2 to 2^-1
+            t[:, 5::8] = 0x78  # 256
+    elif values == "integers that cancel":
+        a, w = _cancelling(gen, M, K), _cancelling(gen, N, K, True)
+    for t in (a, w):
+        t[(t & 0x7F) == 0x7F] = 0  # not a number
+    sa, sw = (torch.exp(torch.randn(s, device="cuda", generator=gen) * 3) for s in ((M, KB), (NB, KB)))
+    out = torch.empty((M, N), dtype=BF16, device="cuda")
+    moe.moe_fp8s_gemm(M, N, K, a, sa, _pack(w[None]), sw, out)
+    torch.cuda.synchronize()
+    x, y = _rows(a, sa), _weights(w, sw)
+    want, size = torch.matmul(x, y.t()), torch.matmul(x.abs(), y.abs().t())
+    lost = torch.zeros_like(want)
+    for k in range(0, K, 8):  # (a block's scales are common to the eight)
+        lost += 7 * 2.0 ** -13 * (x[:, None, k:k + 8] * y[None, :, k:k + 8]).abs().amax(2)
+    # in fp32: sixteen eights of a block, up to three parts of it joined, the scales' product, its product with a block's sum and
+    # the sum over the blocks (k in up to eight parts), each rounded or cut: 2^-23 of the sum of magnitudes
+    bound = lost + size * (16 + 3 + 2 + KB + 8) * 2.0 ** -23
+    assert ((out.double() - want).abs() <= want.abs() * HALF + bound * (1 + HALF)).all()
+
+
 # ---------------------------------------------------------------- fp32 sums
 def _cancelling(gen, n, K, weights=False):
     """Small integers, and in every 128 k the products 256 x 256 and -256 x 256 in two eights, which cancel: an fp32 sum
