@@ -147,3 +147,84 @@ def test_swiglu_of_few_outputs_of_far_rows_sums_in_fp32():
     assert n_src * K > 1 << 32 and 70 * 2 * 128 <= MOST
     for g, (got, gate, up) in enumerate(_grouped(70, 4, 2, 0, 128, K, moe.MOE_ACT_SWIGLU, n_src)):
         assert not _off_by_more(got, gate, up).any(), g
+
+
+# more outputs than SwiGLU's sums are fp32 ones for by themselves: tiles of 64 x 128, of 256 x 256, and far rows
+@pytest.mark.parametrize("T,E,k,ns,N,K,n_src", [(3000, 2, 2, 1, 1024, 272, None), (4500, 2, 2, 0, 2048, 400, None),
+                                                (2100, 40, 3, 1, 1152, 144, None), (2200, 4, 2, 0, 2048, 8208, (1 << 19) + 40)])
+def test_swiglu_f32_sums_in_fp32_at_any_size(T, E, k, ns, N, K, n_src):
+    assert T * (k + ns) * N > MOST
+    for g, (got, gate, up) in enumerate(_grouped(T, E, k, ns, N, K, moe.MOE_ACT_SWIGLU_F32, n_src)):
+        assert not _off_by_more(got, gate, up).any(), g
+
+
+@pytest.mark.parametrize("T,E,k,ns,N,K", FEW)
+def test_swiglu_f32_is_swiglu_where_that_sums_in_fp32(T, E, k, ns, N, K):
+    for (a, _, _), (b, _, _) in zip(_grouped(T, E, k, ns, N, K, moe.MOE_ACT_SWIGLU), _grouped(T, E, k, ns, N, K, moe.MOE_ACT_SWIGLU_F32)):
+        assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- whole experts
+def _definition(layer, x, buf, w13, w2):
+    """The layer's output in 64 bits with the roundings that its definition has: codes of x, h, codes of h, y."""
+    from test_gpu_fp8s import _deq_w, _row_ref
+    d = layer.desc
+    I, H, E, k = d.inter, d.hidden, d.n_routed, d.top_k
+
+    def weights(w, g, N, K):
+        codes = torch.empty((1, N, K), dtype=torch.uint8, device="cuda")
+        scales = torch.empty((1, *_nk(N, K)), device="cuda")
+        moe.moe_fp8s_quant_weights(1, N, K, w[g:g + 1].contiguous(), codes, scales)
+        return _deq_w(codes, scales)[0]
+    xq, idx = _rows(*_row_ref(x)), buf.topk_idx.long()
+    want = torch.zeros((len(x), H), dtype=torch.float64, device="cuda")
+    for e in range(d.groups):
+        t, j = (idx == e).nonzero(as_tuple=True) if e < E else (torch.arange(len(x), device="cuda"), None)
+        if len(t):
+            z = xq[t] @ weights(w13, e, 2 * I, H).t()
+            h = (z[:, :I] / (1 + torch.exp(-z[:, :I])) * z[:, I:]).to(BF16)
+            y = (_rows(*_row_ref(h)) @ weights(w2, e, H, I).t()).to(BF16).double()
+            want.index_add_(0, t, y if j is None else y * buf.topk_w.double()[t, j][:, None])
+    return want
+
+
+# Against the definition an output is off by its own rounding, at most 2^-8 / sqrt(3) of the norm, and by flips of y and of h.  A y
+# whose sum is off by 2^-19 of its terms' sizes (the cut of the down product), 2^-13 of y with terms of random signs, lands
+# beside its value with a chance of 2^-13 / 2^-8 = 2^-5 and is then off by 2^-7 of itself: 2^-7 2^-2.5 = 2^-9.5 at most.  Of fp32
+# sums of gate and up (off by 2^-20 of either, the exponential's 2^-20 too) one h in 2^9 lands beside its bf16 value, one in 16 of those
+# has another code, off by up to 2^-3: 2^-3 2^-6.5 = 2^-9.5 of h.  Together sqrt((2^-8)^2 / 3 + 2 (2^-9.5)^2) = 0.0030.
+@pytest.mark.parametrize("T,H,I,E,k,ns,f32", [(1, 4096, 2048, 8, 6, 1, False), (64, 512, 256, 8, 2, 1, False), (70, 1024, 384, 16, 4, 1, False),
+                                              (600, 512, 512, 12, 3, 1, False), (4000, 512, 2048, 8, 4, 1, True), (2500, 1024, 512, 20, 4, 1, True)])
+def test_layer_of_fp32_sums(T, H, I, E, k, ns, f32):
+    from test_gpu_fp8s import _layer
+    case, layer, buf, w13, w2 = _layer(T, H, I, E, k, ns, T + I)
+    R = layer.desc.rows(T)
+    assert f32 == (T > 64 and R * 2 * I > MOST)
+    layer = moe.MoELayer(layer.desc, layer.w_router, layer.gate_bias, layer.experts, f32_sums=f32)
+    out = layer.forward(case.xd, buf)
+    torch.cuda.synchronize()
+    want = _definition(layer, case.xd, buf, w13, w2)
+    err = float((out.double() - want).norm() / want.norm())
+    say("  out %.2e" % err)
+    assert err <= 0.0030
+
+
+def test_layer_of_fp32_sums_is_the_layer_where_that_sums_in_fp32():
+    from test_gpu_fp8s import _layer
+    for T in (5, 40, 200):
+        case, layer, buf, _, _ = _layer(T, 512, 256, 8, 2, 1, T)
+        other = moe.MoELayer(layer.desc, layer.w_router, layer.gate_bias, layer.experts, f32_sums=True)
+        a = layer.forward(case.xd, buf).clone()
+        assert torch.equal(a, other.forward(case.xd, buf))
+    none = moe.Buffers(layer.desc, 0, fp8s=True)
+    assert other.forward(case.xd[:0], none).shape == (0, 512)
+
+
+def test_refusals():
+    from test_gpu_fp8s import _layer
+    _, layer, buf, w13, w2 = _layer(4, 512, 128, 4, 2, 1, 0)
+    with pytest.raises(ValueError, match="f32_sums"):
+        moe.MoELayer(layer.desc, layer.w_router, layer.gate_bias, moe.bf16_weights(w13, w2), f32_sums=True)
+    with pytest.raises(ValueError, match="out holds"):
+        moe.moe_fp8s_grouped_gemm(layer.desc, 4, buf.xq, buf.xqs, buf.sorted_token, 4, 256, 512, layer.experts.w13, layer.experts.s13,
+                                  buf.group_offsets, moe.MOE_ACT_SWIGLU_F32, buf.h.reshape(-1)[:-1])

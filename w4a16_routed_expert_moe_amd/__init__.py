@@ -2,7 +2,7 @@
 (``include/moe_w4a16.h``), a ctypes binding with the same entry-point names,
 and a thin layer driver.  PyTorch is used for device memory and streams only."""
 from . import _lib
-from ._lib import (MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_DECODE_WORKSPACE_BYTES, MOE_DOWN_COMBINE_MAX_TOKENS,
+from ._lib import (MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_ACT_SWIGLU_F32, MOE_DECODE_WORKSPACE_BYTES, MOE_DOWN_COMBINE_MAX_TOKENS,
                    MOE_TILED_MIN_TOKENS, MoeError, MoeLayerDesc, moe_combine, moe_gen_fp16_scales,
                    moe_gen_int4_codes, moe_permute, moe_route, moe_route_permute, moe_row_sums,
                    moe_w4a16_decode_token, moe_w4a16_decode_token_supported, moe_w4a16_down_combine,
@@ -26,7 +26,7 @@ __all__ = ["moe_act_quant_int8", "moe_w8a8_packed_bytes", "moe_w8a8_prepack", "m
            "moe_act_quant_fp8s", "moe_fp8s_quant_weights", "moe_fp8s_packed_bytes", "moe_fp8s_prepack", "moe_fp8s_gemm",
            "moe_fp8s_linear", "moe_fp8s_grouped_gemm", "moe_fp8s_experts", "quantize_weights_fp8",
            "moe_act_quant_fp8", "moe_act_quant_fp8_dequant", "moe_w4a8_grouped_gemm", "moe_fp8_block_gemm", "moe_fp8_prepack",
-           "moe_workspace_bytes", "moe_route_permute_noalloc", "MOE_ACT_NONE", "MOE_ACT_SWIGLU", "MOE_TILED_MIN_TOKENS", "MoeError", "MoeLayerDesc",
+           "moe_workspace_bytes", "moe_route_permute_noalloc", "MOE_ACT_NONE", "MOE_ACT_SWIGLU", "MOE_ACT_SWIGLU_F32", "MOE_TILED_MIN_TOKENS", "MoeError", "MoeLayerDesc",
            "moe_route", "moe_permute", "moe_route_permute", "moe_w4a16_grouped_gemm", "moe_row_sums",
            "moe_w4a16_down_combine", "MOE_DOWN_COMBINE_MAX_TOKENS", "moe_w4a16_decode_token",
            "moe_w4a16_decode_token_supported", "MOE_DECODE_WORKSPACE_BYTES", "moe_combine", "moe_w4a16_prepack", "moe_gen_int4_codes",

@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_w4a16.so")
 
 MOE_ACT_NONE = 0
 MOE_ACT_SWIGLU = 1
+MOE_ACT_SWIGLU_F32 = 3
 MOE_MAX_TOKENS = 1 << 20
 MOE_TILED_MIN_TOKENS = 384
 MOE_DOWN_COMBINE_MAX_TOKENS = 4
@@ -711,7 +712,7 @@ def moe_fp8s_grouped_gemm(desc: MoeLayerDesc, T: int, a, a_scales, a_gather, n_s
         _at(d, w_packed, "w_packed", _U8, _packed(G, N, K)),
         _at(d, w_scales, "w_scales", _F32, G * _blocks(N) * _blocks(K)),
         _at(d, group_offsets, "group_offsets", _I32, G + 1), act,
-        _at(d, out, "out", _BF16, R * (N // 2 if act == MOE_ACT_SWIGLU else N)), _stream(stream, d)))
+        _at(d, out, "out", _BF16, R * (N // 2 if act in (MOE_ACT_SWIGLU, MOE_ACT_SWIGLU_F32) else N)), _stream(stream, d)))
 
 
 def moe_fp8s_experts(desc: MoeLayerDesc, T: int, x, topk_w, group_offsets, sorted_token, row_of_slot, w13_packed,

@@ -36,6 +36,7 @@ struct Args {
     int KG, NT;              // 128-wide blocks of k, 16-row subtiles per group in the packed weights
     int NB;                  // n-blocks (the instance's tile width)
     int qrows;               // fused quantisation: rows of a tile
+    bool f32;                // SwiGLU: sums in fp32 at any size
 };
 
 // The products of 128 k, without scales (the instruction's own are powers of

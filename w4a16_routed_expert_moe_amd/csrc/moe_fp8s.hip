@@ -408,9 +408,9 @@ extern "C" moe_status moe_fp8s_grouped_gemm(const moe_layer_desc *desc, int32_t 
                                             const int32_t *group_offsets, int32_t act, uint16_t *out, void *stream) {
     MOE_TRY(check_desc(desc));
     MOE_TRY(check_tokens(T));
-    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return MOE_ERR_UNSUPPORTED;
+    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU && act != MOE_ACT_SWIGLU_F32) return MOE_ERR_UNSUPPORTED;
     MOE_TRY(f8::check_nk(N, K));
-    if (act == MOE_ACT_SWIGLU && N % 128) return MOE_ERR_SHAPE;  // both halves whole 64-row tiles
+    if (act != MOE_ACT_NONE && N % 128) return MOE_ERR_SHAPE;  // both halves whole 64-row tiles
     if (a_gather && (n_src < 1 || n_src > MOE_MAX_TOKENS)) return MOE_ERR_SHAPE;
     if (T == 0) return MOE_OK;
     if (!a || !a_scales || !w_packed || !w_scales || !group_offsets || !out) return MOE_ERR_NULL;
@@ -424,7 +424,8 @@ extern "C" moe_status moe_fp8s_grouped_gemm(const moe_layer_desc *desc, int32_t 
     p.gather = a_gather;
     p.n_src = n_src;
     p.offsets = group_offsets;
-    f8::launch_gemm(act, p, T, (hipStream_t)stream);
+    p.f32 = act == MOE_ACT_SWIGLU_F32;
+    f8::launch_gemm(act == MOE_ACT_NONE ? act : MOE_ACT_SWIGLU, p, T, (hipStream_t)stream);
     return launch_status();
 }
 

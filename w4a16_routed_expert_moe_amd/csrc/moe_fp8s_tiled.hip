@@ -475,7 +475,7 @@ bool launch_tiled(int act, Args a, hipStream_t st) {
     // without, 0.0017 with; 8192 tokens 0.0024), and where k in parts leaves the time
     // for them.  800 rows of 41 groups, 1024 x 1024: 13 -> 17 us, 18432 of 257,
     // 4096 x 4096, would be 974 -> 1259.
-    const bool exact = swiglu && (int64_t)a.R * a.N <= 1 << 23;
+    const bool exact = swiglu && (a.f32 || (int64_t)a.R * a.N <= 1 << 23);
     if (a.gather && (int64_t)a.n_src * a.K > kNone) {
         if (exact)
             launch<kSilu, 2, 2, 2, 1, 2, true, true>(a, st);

@@ -12,7 +12,8 @@ own expert format) take moe_mxfp4_decode_token for a single token and
 otherwise moe_mxfp4_grouped_gemm for both GEMMs and the separate combine;
 experts in INT8 (fmt "int8", one scale per output channel) take moe_w8a8_experts
 after the routing; experts in fp8 with an fp32 scale per block of 128 (fmt "fp8")
-take moe_fp8s_experts; experts in bf16 (fmt "bf16") take moe_bf16_experts, and
+take moe_fp8s_experts (with ``f32_sums`` its parts, SwiGLU's sums in fp32 at any
+size); experts in bf16 (fmt "bf16") take moe_bf16_experts, and
 ``MoELayer.backward`` gives their gradients and the router's.  Buffers are allocated once per token count and reused,
 so the sequence can be captured in a HIP graph.
 """
@@ -282,9 +283,12 @@ class MoELayer:
 
     def __init__(self, desc: L.MoeLayerDesc, w_router: torch.Tensor, gate_bias: torch.Tensor,
                  experts: ExpertWeights, fuse_decode: bool = True, fuse_token: bool = True,
-                 w4a8: bool = False):
+                 w4a8: bool = False, f32_sums: bool = False):
         if w4a8 and experts.fmt != "fp4":
             raise ValueError("the W4A8 layer takes FP4 expert weights")
+        if f32_sums and experts.fmt != "fp8":
+            raise ValueError("f32_sums is a choice of the layer with fp8 experts (fmt \"fp8\")")
+        self.f32_sums = f32_sums
         self.w4a8 = w4a8
         self.desc = desc
         self.fuse_decode = fuse_decode
@@ -312,6 +316,15 @@ class MoELayer:
                 raise ValueError("the layer with fp8 experts needs Buffers(..., fp8s=True)")
             L.moe_route_permute(d, T, x, self.w_router, self.gate_bias, buf.logits, buf.topk_idx, buf.topk_w,
                                 buf.group_offsets, buf.sorted_token, buf.row_of_slot, buf.ws, stream)
+            if self.f32_sums and T > 0:
+                L.moe_act_quant_fp8s(T, H, x, buf.xq, buf.xqs, stream)
+                L.moe_fp8s_grouped_gemm(d, T, buf.xq, buf.xqs, buf.sorted_token, T, 2 * I, H, ex.w13, ex.s13,
+                                        buf.group_offsets, L.MOE_ACT_SWIGLU_F32, buf.h, stream)
+                L.moe_act_quant_fp8s(d.rows(T), I, buf.h, buf.hq, buf.hqs, stream)
+                L.moe_fp8s_grouped_gemm(d, T, buf.hq, buf.hqs, None, 0, H, I, ex.w2, ex.s2, buf.group_offsets,
+                                        L.MOE_ACT_NONE, buf.y, stream)
+                L.moe_combine(d, T, buf.y, buf.row_of_slot, buf.topk_w, buf.out, stream)
+                return buf.out
             L.moe_fp8s_experts(d, T, x, buf.topk_w, buf.group_offsets, buf.sorted_token, buf.row_of_slot, ex.w13,
                                ex.s13, ex.w2, ex.s2, buf.xq, buf.xqs, buf.h, buf.hq, buf.hqs, buf.y, buf.out, stream)
             return buf.out
