@@ -198,6 +198,38 @@ def test_gradients_of_groups_without_rows_are_not_touched(N, K, which):
             assert torch.equal(dw[g], torch.matmul(rows["dy"][r].double().t(), rows["a"][r].double()).float()), g
 
 
+@pytest.mark.parametrize("T,H,I,E", [(70, 512, 256, 8), (3000, 512, 4096, 4)])  # tiles of d_h: 128 x 128, 256 x 256
+def test_what_is_not_wanted_is_not_written(T, H, I, E):
+    """Only the routing weights' gradient, or with frozen weights that of the rows: the workspace holds no more than they need."""
+    gen, k = _gen(T), 3
+    desc, R = moe.MoeLayerDesc.make(H, I, E, k, 0), T * k
+    if T == 3000:
+        assert R >= 128 * E and (-(-R // 256) + E // 2) * -(-I // 256) >= 512
+    buf = moe.Buffers(desc, T, train=True)
+    idx = torch.rand((T, E), device="cuda", generator=gen).topk(k, dim=1).indices.to(torch.int32)
+    moe.moe_permute(desc, T, idx, buf.group_offsets, buf.sorted_token, buf.row_of_slot, buf.ws)
+    x, d_out = (torch.randn((T, H), device="cuda", generator=gen).to(BF16) for _ in range(2))
+    w13 = (torch.randn((E, 2 * I, H), device="cuda", generator=gen) / H ** 0.5).to(BF16)
+    w2 = (torch.randn((E, H, I), device="cuda", generator=gen) / I ** 0.5).to(BF16)
+    buf.topk_w.fill_(0.5)
+    moe.moe_bf16_experts(desc, T, x, buf.topk_w, buf.group_offsets, buf.sorted_token, buf.row_of_slot, w13, w2, buf.gu, buf.h, buf.y, buf.out)
+    d2 = torch.empty(w2.shape, device="cuda")
+
+    def written(*outs):
+        buf.grad_ws.fill_(171)
+        moe.moe_bf16_experts_backward(desc, T, d_out, x, buf.topk_w, buf.group_offsets, buf.sorted_token, buf.row_of_slot, w13, w2, buf.gu,
+                                      buf.h, moe.MOE_GRAD_F32, *outs, buf.grad_ws)
+        torch.cuda.synchronize()
+        return int((buf.grad_ws != 171).sum())
+    part, rows_i, rows_h = 4 * R * -(-I // 128), 2 * R * I, 2 * R * H
+    assert written(None, None, None, None) == 0
+    assert 0 < written(None, None, None, buf.d_topk_w) <= part
+    want = buf.d_topk_w.clone()
+    assert rows_i < written(buf.d_x, None, None, buf.d_topk_w) <= part + 2 * rows_i + rows_h
+    assert torch.equal(buf.d_topk_w, want)
+    assert rows_i / 2 < written(None, None, d2, None) <= part + rows_i
+
+
 @pytest.mark.parametrize("T", [6, 300])
 def test_backward_does_not_touch_the_gradients_of_idle_experts(T):
     """The same of the whole backward pass (few tiles: all gradients in one launch; and each in its own)."""

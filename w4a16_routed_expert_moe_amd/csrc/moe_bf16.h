@@ -37,7 +37,7 @@ struct Args {
     const int32_t *row_of_slot;  // [T][k + ns]; row r is one of token gather[r]'s
     const float *topk_w;         // [T][k]
     int k, ns;
-    uint16_t *dgu, *hw;         // [R][2N], [R][N]
+    uint16_t *dgu, *hw;         // [R][2N], [R][N]; null: not wanted
     float *part;                // [NB][R]
     int MB, NB;                 // tiles along M (kTN) and N, set by the launch
 };

@@ -355,6 +355,7 @@ extern "C" moe_status moe_bf16_experts_backward(const moe_layer_desc *desc, int3
             return MOE_ERR_NULL;
         const b16::Workspace at = b16::workspace(desc, T);
         if (ws_bytes < at.bytes) return MOE_ERR_WORKSPACE;
+        if (!d_x && !d_w13 && !d_w2 && !d_topk_w) return MOE_OK;
         char *base = (char *)ws;
         const int R = T * (k + ns);
         float *part = (float *)(base + at.part);
@@ -371,8 +372,8 @@ extern "C" moe_status moe_bf16_experts_backward(const moe_layer_desc *desc, int3
         p.topk_w = topk_w;
         p.k = k;
         p.ns = ns;
-        p.dgu = (uint16_t *)(base + at.dgu);
-        p.hw = (uint16_t *)(base + at.hw);
+        p.dgu = d_x || d_w13 ? (uint16_t *)(base + at.dgu) : nullptr;
+        p.hw = d_w2 ? (uint16_t *)(base + at.hw) : nullptr;
         p.part = part;
         const int NB = b16::launch_wide(b16::kNN, b16::kSwigluBwd, p, st);
         dgu = p.dgu;

@@ -470,11 +470,11 @@ __device__ __forceinline__ void multiply(const Args &p, int block, char *stages)
                         ou[e] = pack_bf16x2(du[0], du[1]);
                         oh[e] = pack_bf16x2(hw[0], hw[1]);
                     }
-                    if (in && n < p.N) {
+                    if (p.dgu && in && n < p.N) {
                         *(u32x4 *)(p.dgu + row * 2 * p.N + n) = og;
                         *(u32x4 *)(p.dgu + row * 2 * p.N + p.N + n) = ou;
-                        *(u32x4 *)(p.hw + row * p.N + n) = oh;
                     }
+                    if (p.hw && in && n < p.N) *(u32x4 *)(p.hw + row * p.N + n) = oh;
                 }
                 dot += __shfl_xor(dot, 16, kWave);
                 dot += __shfl_xor(dot, 32, kWave);
