@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "moe_bf16.h"
+#include "moe_dma.h"
 
 namespace moe {
 namespace b16 {
@@ -28,12 +29,9 @@ constexpr int kBK = 64;  // contraction per step
 // What lanes without an element of a row load.
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};
 
-// A buffer of at most kFar bytes from p: loads from past its end give zeros (no
-// part of an offset is scalar, see moe_dma.h).
-constexpr uint32_t kFar = 0x3FFFFFFFu;
-__device__ __forceinline__ rsrc_t buffer(const void *p, int64_t bytes) {
-    const int n = bytes < 0 ? 0 : bytes > (int64_t)kFar ? (int)kFar : (int)bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, n, 0x00027000);
+// The buffer of moe_dma.h for loads into registers.
+__device__ __forceinline__ rsrc_t resource(const void *p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, buffer_size(bytes), kBufferFlags);
 }
 __device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t voff) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, 0, 0));
@@ -105,8 +103,8 @@ __global__ __launch_bounds__(256, 2) void k_bf16_tiled(Args p) {
     const size_t ld = 2 * (size_t)K;
     const char *w = (const char *)p.b + (size_t)it.g * p.N * ld;
     const int up = (p.N >> 1) + n0;
-    const rsrc_t b0 = buffer(w + n0 * ld, (int64_t)(p.N - n0) * ld);
-    const rsrc_t b1 = EPI == kSwiglu ? buffer(w + up * ld, (int64_t)(p.N - up) * ld) : b0;
+    const rsrc_t b0 = resource(w + n0 * ld, (int64_t)(p.N - n0) * ld);
+    const rsrc_t b1 = EPI == kSwiglu ? resource(w + up * ld, (int64_t)(p.N - up) * ld) : b0;
     const uint32_t voff = (uint32_t)((EPI == kSwiglu ? HS : NSW) * m * ld) + 32 * q;
     auto load_b = [&](u32x4 (&part)[2 * NSW], int kg, int i) {  // half i & 1 of the 32 bytes of subtile i / 2
         const int j = i >> 1;

@@ -12,9 +12,10 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // offset is not below the buffer's size less the scalar offset, which therefore
 // must not lie past the end itself: offsets that may are all in the lanes.
 constexpr uint32_t kFar = 0x3FFFFFFFu;
+constexpr int kBufferFlags = 0x00027000;
+__device__ __forceinline__ int buffer_size(int64_t bytes) { return bytes < 0 ? 0 : bytes > (int64_t)kFar ? (int)kFar : (int)bytes; }
 __device__ __forceinline__ i32x4 buffer(const char *p, int64_t bytes) {
-    const int n = bytes < 0 ? 0 : bytes > (int64_t)kFar ? (int)kFar : (int)bytes;
-    return i32x4{(int)(uint32_t)(uintptr_t)p, (int)((uintptr_t)p >> 32), n, 0x00027000};
+    return i32x4{(int)(uint32_t)(uintptr_t)p, (int)((uintptr_t)p >> 32), buffer_size(bytes), kBufferFlags};
 }
 // 16 bytes per lane straight into LDS, from a buffer or from an address each
 // (see dma16_untracked, also for the wait state; M0 is not restored: nothing
