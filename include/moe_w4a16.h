@@ -61,10 +61,10 @@ typedef enum moe_status {
 
 typedef enum moe_act {
     MOE_ACT_NONE = 0,   /* out = A . W^T                                           */
-    MOE_ACT_SWIGLU = 1, /* W rows [0,N/2) = gate, [N/2,N) = up:                     */
+    MOE_ACT_SWIGLU = 1, /* W rows [0,N/2) = gate, [N/2,N) = up:                    */
                         /* out[:, n] = silu(gate_n) * up_n, N/2 columns            */
-    MOE_ACT_SWIGLU_F32 = 3 /* the same of fp32 sums at any size (moe_fp8s_grouped_ */
-                        /* gemm; elsewhere unsupported)                            */
+    MOE_ACT_SWIGLU_F32 = 3  /* the same of fp32 sums at any size                   */
+                        /* (moe_fp8s_grouped_gemm; unsupported elsewhere)          */
 } moe_act;
 
 /* Shape of one MoE layer.  Limits checked by every call:
@@ -585,17 +585,17 @@ moe_status moe_w8a8_experts(const moe_layer_desc *desc, int32_t T, const uint16_
 /* fp32's range the output does too, or loses digits.  The sums over the     */
 /* blocks are fp32 ones.  Those over the k of a block are the fp8 matrix     */
 /* instruction's: of eight k (8i..8i+7) each product is cut off at 2^-13 of  */
-/* the largest one's power of two (up to 7 * 2^-13 of the largest lost), then */
+/* the largest one's power of two (up to 7/8192 of the largest lost), then   */
 /* they are added in fp32.  Before SwiGLU the products are bf16 ones, whose  */
-/* sums are fp32 throughout (a cut at 2^-24 there), where T <= 64 or R*N <=   */
+/* sums are fp32 throughout (a cut at 2^-24 there), where T <= 64 or R*N <=  */
 /* 2^23, so that h, which is quantised again, is the one of fp32 sums there. */
-/* MOE_ACT_SWIGLU_F32 (moe_fp8s_grouped_gemm) does so at any size; whole       */
-/* experts of it are moe_act_quant_fp8s, that product, moe_act_quant_fp8s,    */
-/* the down product and moe_combine (8192 tokens of 256 experts of 4096/2048: */
-/* 3730 instead of 2140 us, error against 64 bits 0.0017 instead of 0.0024).  */
-/* A token's outputs may differ in their last bits with the size of its batch */
-/* (other tiles add in another order), and, past these bounds, by the cut.    */
-/* Outputs and scratch overlap neither each other nor an input.               */
+/* MOE_ACT_SWIGLU_F32 (moe_fp8s_grouped_gemm) does so at any size; whole     */
+/* experts of it are moe_act_quant_fp8s, that product, moe_act_quant_fp8s,   */
+/* the down product and moe_combine (8192 tokens, 256 experts of 4096/2048:  */
+/* 3730 instead of 2140 us, error against 64 bits 0.0017 instead of 0.0024). */
+/* A token's outputs may differ in their last bits with its batch's size     */
+/* (other tiles add in another order) and, past these bounds, by the cut.    */
+/* Outputs and scratch overlap neither each other nor an input.              */
 
 /* Quantisation of each 128 elements of a row by themselves: with amax the   */
 /* largest |a| of the block,                                                 */

@@ -14,12 +14,15 @@
 // there lets the loads of the step after the next one begin, a whole step
 // before they are needed.
 //
-// Bound by the matrix units' power and issue: 57344 rows of 33 groups of
-// 4096/2048, gate/up 1839 us, 1.05 PFLOP/s, rows' gradient 1604 to 1711, 1.13 to 1.20
-// (matrix units busy 53% at 2.2 GHz), weights' 1930 and 950, 1.0; the library's
-// product of 8192 x 8192 x 8192 does 0.97 to 1.36 in these forms.  SwiGLU's gradient
-// moves 1.4 GB in its epilogue, which a CU's one large tile has nothing to
-// overlap with: 1086 us where the product alone takes 825.
+// 57344 rows of 33 groups of 4096/2048: gate/up 1839 us, 1.05 PFLOP/s, rows'
+// gradient 1604 to 1711, 1.13 to 1.20 (matrix units busy 53% at 2.2 GHz), weights' 1910
+// and 950, 1.0 (44%); the library's product of 8192 x 8192 x 8192 does 0.97 to 1.36 in
+// these forms.  The rest of the matrix units' time goes to what a CU's one large
+// tile has nothing to overlap with, the first loads and the epilogue of each tile,
+// and to waits at the barrier of a step (15 to 18% of the waves' cycles).  SwiGLU's
+// gradient moves 1.4 GB in its epilogue: 1090 us where the product alone takes 825.
+// Gradients added to fp32 read the old values there: the whole backward pass of
+// 8192 tokens on these experts takes 5770 us with them in bf16, 6010 in fp32, 6940 added.
 #include <algorithm>
 #include <type_traits>
 

@@ -57,7 +57,9 @@ __device__ __forceinline__ v8i join(u32x4 lo, u32x4 hi) {
 // the next product.  That adds as much to the error of a layer's output as its
 // bf16 rounding does (0.0017 -> 0.0024 of its norm), and more where few values
 // make up the output.  The products that SwiGLU follows are therefore these
-// where its outputs are few (launch_tiled) and in the weight stream.
+// where its outputs are few (launch_tiled), in the weight stream, and where the
+// caller asks for them (they take twice the matrix instructions' time and the
+// conversions).
 __device__ __forceinline__ bf16x8 to_bf16(int lo, int hi) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);

@@ -33,7 +33,8 @@ __global__ __launch_bounds__(256) void k_act_quant_fp8s(const uint16_t *__restri
     if ((c & 15) == 0) scales[(size_t)row * KG + (c >> 4)] = s.scale;
 }
 
-// A workgroup per block of 128 x 128 weights.
+// A workgroup per block of 128 x 128 weights.  Bound by HBM: 257 x 4096 x 4096 in
+// 2425 us, 5.3 TB/s; 4096 x 4096 in 11.9.
 __global__ __launch_bounds__(256) void k_weight_quant_fp8s(const uint16_t *__restrict__ w, int N, int K, int NBK, int KG,
                                                            uint8_t *__restrict__ codes, float *__restrict__ scales) {
     __shared__ uint32_t smax[4];

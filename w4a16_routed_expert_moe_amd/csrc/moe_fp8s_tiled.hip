@@ -13,11 +13,14 @@
 // there lets the loads of the step after the next begin; the weights' registers are
 // read anew, for the next step, as each has served the last two.
 //
-// Bound by power and by the vector units, which have four multiply-adds for each
-// matrix instruction (34 cycles the pair): 8192 x 4096 x 4096 124 us, 20 in a row 137
-// to 142, 1.95 to 2.2 PFLOP/s at 2.08 GHz with the matrix units busy 53%; 57344
-// rows of 33 groups, gate/up 991 to 1114 us, 1.7 to 1.9.  Few rows of many
-// weights: HBM, 5.7 TB/s.
+// 8192 x 4096 x 4096 124 us, 20 in a row 137 to 142, 1.95 to 2.2 PFLOP/s; 57344 rows of
+// 33 groups, gate/up 991 to 1114 us, 1.7 to 1.9.  The matrix units are busy 53% of
+// that at 2.08 GHz, the waves wait for 24% of their cycles and bank conflicts take
+// 12% of those in which LDS works: the eight waves of the one workgroup on a CU
+// meet at a barrier every step and read LDS at the same time.  The four
+// multiply-adds for each matrix instruction cost a cycle of its 33 where only they
+// run; without them the kernel takes 105 us.  Few rows of many weights: HBM, 5.7
+// TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -474,7 +477,8 @@ bool launch_tiled(int act, Args a, hipStream_t st) {
     // up (64 tokens of the 256-expert layer: error against 64 bits 0.0020 to 0.0033
     // without, 0.0017 with; 8192 tokens 0.0024), and where k in parts leaves the time
     // for them.  800 rows of 41 groups, 1024 x 1024: 13 -> 17 us, 18432 of 257,
-    // 4096 x 4096, would be 974 -> 1259.
+    // 4096 x 4096, would be 974 -> 1259.  (MOE_ACT_SWIGLU_F32: always; 8192 tokens of the
+    // 256-expert layer 2140 -> 3730.)
     const bool exact = swiglu && (a.f32 || (int64_t)a.R * a.N <= 1 << 23);
     if (a.gather && (int64_t)a.n_src * a.K > kNone) {
         if (exact)
