@@ -5,12 +5,11 @@ is how most kernels here issue loads into LDS.  Every source is compiled with th
 neither may occur (CPU only)."""
 import os
 import re
-import subprocess
-from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
-HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+from compiled_sources import HIPCC, all_assembly
+
 pytestmark = pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not found")
 
 
@@ -83,19 +82,8 @@ def test_finds_a_load_without_wait():
 
 
 @pytest.fixture(scope="module")
-def compiled(tmp_path_factory):
-    from w4a16_routed_expert_moe_amd import build as b
-    d = tmp_path_factory.mktemp("asm")
-
-    def one(src):
-        out = str(d / (src + ".s"))
-        flags = [f for f in b.FLAGS if f != "-fPIC"] + b.EXTRA.get(src, [])
-        r = subprocess.run([HIPCC] + flags + ["--cuda-device-only", "-S", "-o", out, os.path.join(b.CSRC, src)],
-                           capture_output=True, text=True)
-        assert r.returncode == 0, r.stderr
-        return open(out).read().splitlines()
-    with ThreadPoolExecutor(max_workers=4) as ex:
-        return dict(zip(b.SOURCES, ex.map(one, b.SOURCES)))
+def compiled():
+    return all_assembly()
 
 
 def test_no_load_into_lds_follows_a_write_of_m0(compiled):
