@@ -723,6 +723,7 @@ moe_status moe_bf16_grouped_dgrad(const moe_layer_desc *desc, int32_t T, const u
 /*   mode       MOE_GRAD_BF16: dw bf16 [G][N][K], written (zeros for a group */
 /*              without rows, and with T = 0); MOE_GRAD_F32: the same in     */
 /*              fp32; MOE_GRAD_F32_ADD: added to the fp32 values there       */
+/*              (those of a group without rows are neither read nor written) */
 /*   dw         16-byte aligned                                              */
 #define MOE_GRAD_BF16 0
 #define MOE_GRAD_F32 1

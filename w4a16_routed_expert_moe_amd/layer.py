@@ -316,7 +316,7 @@ class MoELayer:
                 raise ValueError("the layer with fp8 experts needs Buffers(..., fp8s=True)")
             L.moe_route_permute(d, T, x, self.w_router, self.gate_bias, buf.logits, buf.topk_idx, buf.topk_w,
                                 buf.group_offsets, buf.sorted_token, buf.row_of_slot, buf.ws, stream)
-            if self.f32_sums and T > 0:
+            if self.f32_sums and T > 64 and d.rows(T) * 2 * I > 1 << 23:  # (else moe_fp8s_experts sums in fp32 itself)
                 L.moe_act_quant_fp8s(T, H, x, buf.xq, buf.xqs, stream)
                 L.moe_fp8s_grouped_gemm(d, T, buf.xq, buf.xqs, buf.sorted_token, T, 2 * I, H, ex.w13, ex.s13,
                                         buf.group_offsets, L.MOE_ACT_SWIGLU_F32, buf.h, stream)
